@@ -298,6 +298,101 @@ int moe_finalize(const void* stage, int T, int k, int H, void* out, void* stream
 int moe_cast_e4m3(const void* x, int T, int H, uint8_t* codes, uint8_t* scales, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * Residual addition + root-mean-square norm, in front of the layer.
+ *   s = x + residual (32 bits; s = x when residual is NULL)
+ *   residual_out = s rounded to residual_dt
+ *   y = s * rsqrt(mean_h(s^2) + eps) * weight, from the unrounded s
+ * and y leaves the kernel as bf16 rows (what the router and bf16 experts
+ * read), as e4m3 codes with UE8M0 scales (what low-bit experts read: the
+ * format of moe_cast_e4m3, one scale per 32 values, the smallest 2^p with
+ * amax / 2^p <= 448), or as both.  The codes are rounded once, from the
+ * 32-bit y, not from its bf16 rounding.
+ *   x            [T,H] x_dt: BF16 or F32
+ *   residual     [T,H] residual_dt: BF16 or F32, or NULL (then residual_out
+ *                must be NULL and residual_dt is ignored)
+ *   weight       [H] weight_dt: BF16 or F32
+ *   residual_out [T,H] residual_dt; may be residual itself (in place), no
+ *                other overlap of outputs and inputs is allowed
+ *   y            [T,H] bf16 out, or NULL
+ *   codes        [T,H] e4m3 out and scales [T,H/32] UE8M0 out, or both NULL
+ * Limits: eps >= 0; at least one of y and codes; every pointer aligned to its
+ * element; with codes H % 32 == 0 and every pointer but scales 16-byte
+ * aligned.  Any H >= 1 otherwise.  A row that holds a NaN or an infinity
+ * gives NaN where the formula does.  One launch, no workspace.
+ * ------------------------------------------------------------------------- */
+int moe_add_rms_norm(const void* x, int x_dt, const void* residual, int residual_dt,
+                     const void* weight, int weight_dt, float eps, int T, int H,
+                     void* residual_out, void* y, uint8_t* codes, uint8_t* scales, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Dense matrix product with bias, activation and residual in its epilogue:
+ * the shared expert beside the routed ones, the gate's logits in 32 bits.
+ *   v   = x w^T + bias                     (exact products, 32-bit sums)
+ *   out = act(v) + residual, rounded once to out_dt
+ *   x        [T,K] bf16
+ *   w        [N,K] bf16; with MOE_ACT_SWIGLU [2N,K], the N gate rows first,
+ *            then the N up rows (the order of w13)
+ *   bias     fp32 [N] (swiglu [2N]), or NULL
+ *   act      MOE_ACT_NONE, _SILU (v / (1 + e^-v)), _GELU (v * Phi(v), the
+ *            error-function form), _SWIGLU (silu(v_gate) * v_up)
+ *   residual [T,N] residual_dt: BF16 or F32, or NULL; may be out itself when
+ *            the types agree
+ *   out      [T,N] out_dt: BF16 or F32
+ * Limits: K % 8 == 0; x and w 16-byte aligned, the others to their element;
+ * N >= 1 and T >= 0 of any size with (2)N, T and K below 2^31.  Workspace of
+ * moe_linear_workspace_bytes (the common rules above).
+ * ------------------------------------------------------------------------- */
+typedef enum {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_SILU = 1,
+  MOE_ACT_GELU = 2,
+  MOE_ACT_SWIGLU = 3
+} moe_activation;
+size_t moe_linear_workspace_bytes(int T, int K, int N, int act);
+int moe_linear(const void* x, const void* w, const float* bias, int act, const void* residual,
+               int residual_dt, int T, int K, int N, void* out, int out_dt, void* ws,
+               size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Expert-load balance loss, per-expert counts and the gradient of the logits.
+ * For sequence b with n_b counted tokens and c_be assignments to expert e:
+ *   f_be = E c_be / sum_e c_be         the expert's share of the load (1 = even)
+ *   p_te = softmax(l_t)_e, or s_te / (sum_e s_te + 1e-20) with the sigmoid or
+ *          sqrt-softplus scores s of moe_router
+ *   L    = coef / B' * sum_b (1/n_b) sum_t sum_e f_be p_te
+ * with B' the sequences that hold a counted token (the others add nothing;
+ * L = 0 when there are none).  f is a constant of the gradient:
+ *   dL/dl_te = coef / (B' n_b) * d_te * (f_be - sum_j f_bj p_tj)
+ * with d = p (softmax) or s'(l) / (sum s + 1e-20).  A softmax row whose
+ * logits are all -inf has p = 0.
+ *   logits     [T,E] logits_dt: F32 or BF16 (before the selection bias)
+ *   topk_ids   [T,k] int32, as moe_router wrote them.  An id outside [0,E) is
+ *              not counted and sets MOE_DEVERR_BAD_EXPERT_ID.
+ *   token_mask [T] bytes, zero = not counted (padding), or NULL
+ *   seq_starts [B+1] int32, ascending: sequence b is tokens [seq_starts[b],
+ *              seq_starts[b+1]); or NULL: one sequence of all tokens (B = 1).
+ *              Tokens outside every sequence are not counted.
+ *   loss       [1] fp32 out
+ *   counts     [B,E] int32 out (c_be), tokens [B] int32 out (n_b)
+ *   dlogits    [T,E] logits_dt out: the gradient of L, zero for tokens that
+ *              are not counted; or NULL for the loss and counts alone
+ * moe_balance_loss_backward gives dlogits = *dloss * dL/dl from the counts
+ * and tokens of a forward call on the same arguments (dloss: fp32 [1], device).
+ * Sums of many tokens are in 64 bits and in a fixed order: the same inputs
+ * give the same bits.
+ * Limits: 1 <= k <= min(E,16), E <= 512, 1 <= B <= 65536, T*k and B*E below 2^31.
+ * ------------------------------------------------------------------------- */
+size_t moe_balance_loss_workspace_bytes(int T, int E, int B);
+int moe_balance_loss(const void* logits, int logits_dt, const int32_t* topk_ids,
+                     const uint8_t* token_mask, const int32_t* seq_starts, int B, int T, int E,
+                     int k, int scoring, float coef, float* loss, int32_t* counts,
+                     int32_t* tokens, void* dlogits, void* ws, size_t ws_bytes, void* stream);
+int moe_balance_loss_backward(const float* dloss, const void* logits, int logits_dt,
+                              const int32_t* counts, const int32_t* tokens,
+                              const uint8_t* token_mask, const int32_t* seq_starts, int B, int T,
+                              int E, int scoring, float coef, void* dlogits, void* stream);
+
+/* ---------------------------------------------------------------------------
  * The whole layer: router, align, GEMM1 + SwiGLU, GEMM2 + weight, finalize,
  * enqueued back to back with no host synchronisation.  block_m = 0 picks the
  * tile height from the mean rows per expert T*k/E: 16 below 8, 64 below 64,

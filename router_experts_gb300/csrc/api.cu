@@ -584,6 +584,139 @@ int moe_cast_e4m3(const void* x, int T, int H, uint8_t* codes, uint8_t* scales, 
   return MOE_OK;
 }
 
+// ---- norm -------------------------------------------------------------------------
+static bool float_dt(int dt) { return dt == MOE_DT_BF16 || dt == MOE_DT_F32; }
+static size_t dt_size(int dt) { return dt == MOE_DT_F32 ? 4 : 2; }
+
+int moe_add_rms_norm(const void* x, int x_dt, const void* residual, int residual_dt,
+                     const void* weight, int weight_dt, float eps, int T, int H,
+                     void* residual_out, void* y, uint8_t* codes, uint8_t* scales,
+                     void* stream) {
+  if (!float_dt(x_dt) || !float_dt(weight_dt) || (residual && !float_dt(residual_dt)))
+    return MOE_ERR_UNSUPPORTED;
+  if (T < 0 || H <= 0 || !(eps >= 0.f)) return MOE_ERR_ARG;
+  if ((codes == nullptr) != (scales == nullptr) || (codes && H % 32 != 0)) return MOE_ERR_ARG;
+  if (T == 0) return MOE_OK;
+  if (!x || !weight || (!y && !codes)) return MOE_ERR_ARG;
+  if ((residual == nullptr) != (residual_out == nullptr)) return MOE_ERR_ARG;
+  const size_t rs = residual ? dt_size(residual_dt) : 1;
+  if (!aligned(x, dt_size(x_dt)) || !aligned(weight, dt_size(weight_dt)) ||
+      !aligned(residual, rs) || !aligned(residual_out, rs) || !aligned(y, 2))
+    return MOE_ERR_ARG;
+  const bool vec = H % 8 == 0 && aligned(x, 16) && aligned(weight, 16) && aligned(residual, 16) &&
+                   aligned(residual_out, 16) && aligned(y, 16) && aligned(codes, 16);
+  if (codes && !vec) return MOE_ERR_ARG;
+  if (launch_add_rms_norm(x, x_dt == MOE_DT_F32, residual, residual_dt == MOE_DT_F32, weight,
+                          weight_dt == MOE_DT_F32, eps, T, H, residual_out, y, codes, scales, vec,
+                          static_cast<cudaStream_t>(stream)) != 0)
+    return launch_fail("norm kernel");
+  return MOE_OK;
+}
+
+// ---- dense product ------------------------------------------------------------------
+static bool linear_shape(int T, int K, int N, int act) {
+  if (T < 0 || K <= 0 || N <= 0 || K % 8 != 0) return false;
+  if (act < MOE_ACT_NONE || act > MOE_ACT_SWIGLU) return false;
+  return act != MOE_ACT_SWIGLU || N <= 0x3fffffff;
+}
+
+size_t moe_linear_workspace_bytes(int T, int K, int N, int act) {
+  if (!linear_shape(T, K, N, act)) return 0;
+  const int sms = device_num_sms() > 0 ? device_num_sms() : 152;
+  return kWsHeaderBytes + plan_linear(T, K, N, act == MOE_ACT_SWIGLU, sms).partial_bytes;
+}
+
+int moe_linear(const void* x, const void* w, const float* bias, int act, const void* residual,
+               int residual_dt, int T, int K, int N, void* out, int out_dt, void* ws,
+               size_t ws_bytes, void* stream) {
+  if (!linear_shape(T, K, N, act)) return MOE_ERR_ARG;
+  if (!float_dt(out_dt) || (residual && !float_dt(residual_dt))) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!x || !w || !out || !ws) return MOE_ERR_ARG;
+  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(bias, 4) || !aligned(out, dt_size(out_dt)) ||
+      (residual && !aligned(residual, dt_size(residual_dt))) || !aligned(ws, 256))
+    return MOE_ERR_ARG;
+  const int sms = device_num_sms();
+  if (sms <= 0) return cuda_fail("cudaDeviceGetAttribute", cudaGetLastError());
+  const LinearPlan plan = plan_linear(T, K, N, act == MOE_ACT_SWIGLU, sms);
+  if (ws_bytes < kWsHeaderBytes + plan.partial_bytes) return MOE_ERR_ARG;
+  char* base = static_cast<char*>(ws);
+  const char* why = "";
+  if (launch_linear(x, w, bias, act, residual, residual_dt == MOE_DT_F32, T, K, N, out,
+                    out_dt == MOE_DT_F32, plan, reinterpret_cast<float*>(base + kWsHeaderBytes),
+                    reinterpret_cast<int*>(base + kWsFfnTicketOffset), err_word(ws), sms,
+                    static_cast<cudaStream_t>(stream), &why) != 0)
+    return launch_fail(why);
+  return MOE_OK;
+}
+
+// ---- balance loss ---------------------------------------------------------------------
+static int check_balance(const void* logits, int logits_dt, const int32_t* seq_starts, int B,
+                         int T, int E, int scoring, float coef) {
+  if (logits_dt != MOE_DT_F32 && logits_dt != MOE_DT_BF16) return MOE_ERR_UNSUPPORTED;
+  if (T < 0 || E <= 0 || E > 512 || B < 1 || B > 65536 || coef != coef) return MOE_ERR_ARG;
+  if (!seq_starts && B != 1) return MOE_ERR_ARG;
+  if (scoring != MOE_SCORING_SOFTMAX && scoring != MOE_SCORING_SIGMOID &&
+      scoring != MOE_SCORING_SQRT_SOFTPLUS)
+    return MOE_ERR_ARG;
+  if (T > 0 && (!logits || !aligned(logits, dt_size(logits_dt)))) return MOE_ERR_ARG;
+  if (seq_starts && !aligned(seq_starts, 4)) return MOE_ERR_ARG;
+  return MOE_OK;
+}
+// four experts a load: whole groups of four, each at its own alignment
+static bool balance_vec(const void* logits, const void* dlogits, int logits_dt, int E) {
+  const size_t a = 4 * dt_size(logits_dt);
+  return E % 4 == 0 && aligned(logits, a) && aligned(dlogits, a);
+}
+
+size_t moe_balance_loss_workspace_bytes(int T, int E, int B) {
+  if (T < 0 || E <= 0 || E > 512 || B < 1 || B > 65536) return 0;
+  return kWsHeaderBytes + align_up(static_cast<size_t>(balance_grid(T)) * 8, 256);
+}
+
+int moe_balance_loss(const void* logits, int logits_dt, const int32_t* topk_ids,
+                     const uint8_t* token_mask, const int32_t* seq_starts, int B, int T, int E,
+                     int k, int scoring, float coef, float* loss, int32_t* counts,
+                     int32_t* tokens, void* dlogits, void* ws, size_t ws_bytes, void* stream) {
+  const int rc = check_balance(logits, logits_dt, seq_starts, B, T, E, scoring, coef);
+  if (rc != MOE_OK) return rc;
+  if (k < 1 || k > E || k > 16 || static_cast<long long>(T) * k > 0x7fffffffll)
+    return MOE_ERR_ARG;
+  if (!loss || !counts || !tokens || !ws || (T > 0 && !topk_ids)) return MOE_ERR_ARG;
+  if (!aligned(loss, 4) || !aligned(counts, 4) || !aligned(tokens, 4) || !aligned(topk_ids, 4) ||
+      !aligned(dlogits, dt_size(logits_dt)) || !aligned(ws, 256))
+    return MOE_ERR_ARG;
+  if (ws_bytes < moe_balance_loss_workspace_bytes(T, E, B)) return MOE_ERR_ARG;
+  char* base = static_cast<char*>(ws);
+  if (launch_balance_loss(logits, logits_dt == MOE_DT_BF16, topk_ids, token_mask, seq_starts, B, T,
+                          E, k, scoring, coef, loss, counts, tokens, dlogits,
+                          balance_vec(logits, dlogits, logits_dt, E),
+                          reinterpret_cast<double*>(base + kWsHeaderBytes),
+                          reinterpret_cast<int*>(base + kWsBalanceTicketOffset), err_word(ws),
+                          static_cast<cudaStream_t>(stream)) != 0)
+    return launch_fail("balance loss kernel");
+  return MOE_OK;
+}
+
+int moe_balance_loss_backward(const float* dloss, const void* logits, int logits_dt,
+                              const int32_t* counts, const int32_t* tokens,
+                              const uint8_t* token_mask, const int32_t* seq_starts, int B, int T,
+                              int E, int scoring, float coef, void* dlogits, void* stream) {
+  const int rc = check_balance(logits, logits_dt, seq_starts, B, T, E, scoring, coef);
+  if (rc != MOE_OK) return rc;
+  if (T == 0) return MOE_OK;
+  if (!dloss || !counts || !tokens || !dlogits) return MOE_ERR_ARG;
+  if (!aligned(dloss, 4) || !aligned(counts, 4) || !aligned(tokens, 4) ||
+      !aligned(dlogits, dt_size(logits_dt)))
+    return MOE_ERR_ARG;
+  if (launch_balance_loss_backward(dloss, logits, logits_dt == MOE_DT_BF16, counts, tokens,
+                                   token_mask, seq_starts, B, T, E, scoring, coef, dlogits,
+                                   balance_vec(logits, dlogits, logits_dt, E),
+                                   static_cast<cudaStream_t>(stream)) != 0)
+    return launch_fail("balance loss gradient kernel");
+  return MOE_OK;
+}
+
 // ---- layer ------------------------------------------------------------------------
 size_t moe_layer_workspace_bytes(int T, int H, int F, int E, int k, int block_m, int act_dt) {
   if (T < 0 || H <= 0 || F <= 0 || E <= 0 || k <= 0) return 0;

@@ -367,15 +367,37 @@ MOE_DEV uint32_t pack_bf16x2(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
-// FP8 cast of 32 consecutive bf16 values ("How GPUs Fuse Communication and
-// Computation During LLM Inference" §1.1 and the scale rule of §3.5): 2^s is
-// the smallest power of two with amax / 2^s <= 448 (s in [-127, 127]; 0 for
-// an all-zero group), codes = e4m3(v / 2^s), nearest, ties to even,
-// saturating; the scale byte is s + 127 (UE8M0).  s comes from amax's binary
-// exponent, not from a rounded quotient: amax = m * 2^e with m in [0.5, 1)
-// and 448 = 0.875 * 2^9, so amax <= 448 * 2^s exactly when s >= e - 9
-// (m <= 0.875) or s >= e - 8 (m > 0.875).  src: four 16-byte words (64
-// bytes), dst: two 16-byte words of codes.
+// Scale rule of the FP8 cast ("How GPUs Fuse Communication and Computation
+// During LLM Inference" §1.1 and §3.5): 2^s is the smallest power of two with
+// amax / 2^s <= 448 (s in [-127, 127]; 0 for an all-zero group).  s comes
+// from amax's binary exponent, not from a rounded quotient: amax = m * 2^e
+// with m in [0.5, 1) and 448 = 0.875 * 2^9, so amax <= 448 * 2^s exactly when
+// s >= e - 9 (m <= 0.875) or s >= e - 8 (m > 0.875).  *mul = 2^-s, exactly
+// (2^127 at most; 2^-127 is the subnormal 0x00400000).
+MOE_DEV int e4m3_scale_exponent(float amax, float* mul) {
+  int s = 0;
+  if (amax > 0.f) {
+    int e;
+    const float m = frexpf(amax, &e);
+    s = (m <= 0.875f) ? e - 9 : e - 8;
+    s = max(-127, min(127, s));
+  }
+  *mul = (s <= 126) ? __int_as_float((127 - s) << 23) : __int_as_float(0x00400000);
+  return s;
+}
+
+// Four e4m3 codes, nearest, ties to even, saturating.
+MOE_DEV uint32_t pack_e4m3x4(float a, float b, float c, float d) {
+  const __nv_fp8x2_storage_t lo =
+      __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const __nv_fp8x2_storage_t hi =
+      __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+  return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+}
+
+// FP8 cast of 32 consecutive bf16 values: codes = e4m3(v / 2^s), the scale
+// byte is s + 127 (UE8M0).  src: four 16-byte words (64 bytes), dst: two
+// 16-byte words of codes.
 MOE_DEV void cast_e4m3_group32(const uint4* __restrict__ src, uint4* __restrict__ dst,
                                uint8_t* __restrict__ scale) {
   uint4 raw[4];
@@ -394,24 +416,12 @@ MOE_DEV void cast_e4m3_group32(const uint4* __restrict__ src, uint4* __restrict_
   }
 #pragma unroll
   for (int i = 0; i < 32; ++i) amax = fmaxf(amax, fabsf(v[i]));
-  int s = 0;
-  if (amax > 0.f) {
-    int e;
-    const float m = frexpf(amax, &e);
-    s = (m <= 0.875f) ? e - 9 : e - 8;
-    s = max(-127, min(127, s));
-  }
-  // 2^-s exactly (2^127 at most; 2^-127 is the subnormal 0x00400000)
-  const float mul = (s <= 126) ? __int_as_float((127 - s) << 23) : __int_as_float(0x00400000);
+  float mul;
+  const int s = e4m3_scale_exponent(amax, &mul);
   uint32_t c[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(
-        make_float2(v[4 * i] * mul, v[4 * i + 1] * mul), __NV_SATFINITE, __NV_E4M3);
-    const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(
-        make_float2(v[4 * i + 2] * mul, v[4 * i + 3] * mul), __NV_SATFINITE, __NV_E4M3);
-    c[i] = static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
-  }
+  for (int i = 0; i < 8; ++i)
+    c[i] = pack_e4m3x4(v[4 * i] * mul, v[4 * i + 1] * mul, v[4 * i + 2] * mul, v[4 * i + 3] * mul);
   dst[0] = make_uint4(c[0], c[1], c[2], c[3]);
   dst[1] = make_uint4(c[4], c[5], c[6], c[7]);
   *scale = static_cast<uint8_t>(s + 127);

@@ -21,6 +21,7 @@ constexpr size_t kWsAlignBarrierOffset = 5120;      // int32[2] grid barrier of 
 constexpr size_t kWsAlignTicketOffset = 5128;       // int32 align: CTAs done reading the counts
 constexpr size_t kWsWaitLimitOffset = 5376;         // int64 test hook: align barrier limit (cycles)
 constexpr size_t kWsDecodeCounterOffset = 6144;     // int32[3] persistent layer: routed, zeroed, done
+constexpr size_t kWsBalanceTicketOffset = 6400;     // int32 balance loss: CTAs done
 constexpr size_t kWsRouterTicketOffset = 8192;      // int32[kRouterMaxTiles]
 constexpr int kRouterMaxTiles = 65536;              // token tiles of 16 -> T <= 1,048,576
 constexpr size_t kWsAlignHistOffset = kWsRouterTicketOffset + 4ull * kRouterMaxTiles;
@@ -191,6 +192,45 @@ int launch_decode_layer(const void* hidden, const void* gate, const float* bias,
                         int32_t* topk_ids, float* topk_weights, char* region,
                         int* router_tickets, int* counters, int* err, const DecodePlan& d,
                         int num_sms, cudaStream_t stream);
+
+// ---- norm (norm.cu) ---------------------------------------------------------------
+// vec: H % 8 == 0 and every pointer but scales 16-byte aligned.  res may be
+// nullptr (then res_out is unused); codes need vec and H % 32 == 0.
+int launch_add_rms_norm(const void* x, int x_f32, const void* res, int res_f32, const void* w,
+                        int w_f32, float eps, int T, int H, void* res_out, void* y,
+                        uint8_t* codes, uint8_t* scales, bool vec, cudaStream_t stream);
+
+// ---- dense product (linear.cu) ------------------------------------------------------
+struct LinearPlan {
+  int bn;         // token columns of a tile
+  int tiles_n;    // weight tiles of 128 output columns
+  int tiles_t;    // token tiles
+  int splits;     // K splits of a tile
+  size_t partial_bytes;
+};
+LinearPlan plan_linear(int T, int K, int N, bool gated, int num_sms);
+int launch_linear(const void* x, const void* w, const float* bias, int act, const void* residual,
+                  int residual_f32, int T, int K, int N, void* out, int out_f32,
+                  const LinearPlan& plan, float* partial, int* tickets, int* err, int num_sms,
+                  cudaStream_t stream, const char** why);
+
+// ---- balance loss (balance.cu) --------------------------------------------------------
+// CTAs of the token kernel: eight tokens in flight a CTA, four CTAs an SM.
+inline int balance_grid(int T) {
+  const int g = (T + 7) / 8;
+  return g < 608 ? g : 608;
+}
+// vec: E % 4 == 0 and logits / dlogits aligned to four elements.  part:
+// balance_grid(T) doubles; ticket: zero before the first call.
+int launch_balance_loss(const void* logits, bool bf16, const int32_t* ids, const uint8_t* mask,
+                        const int32_t* starts, int B, int T, int E, int k, int scoring,
+                        float coef, float* loss, int32_t* counts, int32_t* tokens, void* dlogits,
+                        bool vec, double* part, int* ticket, int* err, cudaStream_t st);
+int launch_balance_loss_backward(const float* dloss, const void* logits, bool bf16,
+                                 const int32_t* counts, const int32_t* tokens,
+                                 const uint8_t* mask, const int32_t* starts, int B, int T, int E,
+                                 int scoring, float coef, void* dlogits, bool vec,
+                                 cudaStream_t st);
 
 // ---- floor probes (measurement) -------------------------------------------------
 int launch_probe_empty(int blocks, int threads, cudaStream_t stream);
