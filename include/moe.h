@@ -340,7 +340,8 @@ int moe_add_rms_norm(const void* x, int x_dt, const void* residual, int residual
  *   out      [T,N] out_dt: BF16 or F32
  * Limits: K % 8 == 0; x and w 16-byte aligned, the others to their element;
  * N >= 1 and T >= 0 of any size with (2)N, T and K below 2^31.  Workspace of
- * moe_linear_workspace_bytes (the common rules above).
+ * moe_linear_workspace_bytes (the header only: partial sums meet in shared
+ * memory; the common rules above).
  * ------------------------------------------------------------------------- */
 typedef enum {
   MOE_ACT_NONE = 0,

@@ -622,8 +622,7 @@ static bool linear_shape(int T, int K, int N, int act) {
 
 size_t moe_linear_workspace_bytes(int T, int K, int N, int act) {
   if (!linear_shape(T, K, N, act)) return 0;
-  const int sms = device_num_sms() > 0 ? device_num_sms() : 152;
-  return kWsHeaderBytes + plan_linear(T, K, N, act == MOE_ACT_SWIGLU, sms).partial_bytes;
+  return kWsHeaderBytes;
 }
 
 int moe_linear(const void* x, const void* w, const float* bias, int act, const void* residual,
@@ -634,18 +633,16 @@ int moe_linear(const void* x, const void* w, const float* bias, int act, const v
   if (T == 0) return MOE_OK;
   if (!x || !w || !out || !ws) return MOE_ERR_ARG;
   if (!aligned(x, 16) || !aligned(w, 16) || !aligned(bias, 4) || !aligned(out, dt_size(out_dt)) ||
-      (residual && !aligned(residual, dt_size(residual_dt))) || !aligned(ws, 256))
+      (residual && !aligned(residual, dt_size(residual_dt))) || !aligned(ws, 256) ||
+      ws_bytes < kWsHeaderBytes)
     return MOE_ERR_ARG;
   const int sms = device_num_sms();
   if (sms <= 0) return cuda_fail("cudaDeviceGetAttribute", cudaGetLastError());
   const LinearPlan plan = plan_linear(T, K, N, act == MOE_ACT_SWIGLU, sms);
-  if (ws_bytes < kWsHeaderBytes + plan.partial_bytes) return MOE_ERR_ARG;
-  char* base = static_cast<char*>(ws);
   const char* why = "";
   if (launch_linear(x, w, bias, act, residual, residual_dt == MOE_DT_F32, T, K, N, out,
-                    out_dt == MOE_DT_F32, plan, reinterpret_cast<float*>(base + kWsHeaderBytes),
-                    reinterpret_cast<int*>(base + kWsFfnTicketOffset), err_word(ws), sms,
-                    static_cast<cudaStream_t>(stream), &why) != 0)
+                    out_dt == MOE_DT_F32, plan, err_word(ws), sms, static_cast<cudaStream_t>(stream),
+                    &why) != 0)
     return launch_fail(why);
   return MOE_OK;
 }

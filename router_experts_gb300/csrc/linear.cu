@@ -1,22 +1,30 @@
 // linear.cu -- dense product with bias, activation and residual in its
 // epilogue:  out[t, n] = act(sum_k x[t, k] w[n, k] + bias[n]) + residual[t, n].
 //
-// Tiles put the weights on the MMA's 128 rows (TMEM lanes) and the tokens on
-// its columns: a thread of the epilogue owns one output column n and walks
-// the tile's tokens, so the 32 lanes of a warp touch 32 neighbouring outputs
-// of one token whatever N's alignment, and one token costs a tile of 16
-// columns and not of 128.  A gated tile (swiglu) takes the 128 gate rows and
-// the matching 128 up rows into two accumulators, which the same thread reads.
+// Three kernels, by the number of tokens and an estimate of their time
+// (plan_linear):
 //
-// One persistent kernel, six warps:
-//   warp 0     TMA producer into a ring of 64-wide K steps
-//   warp 1     TMEM allocator; one thread issues tcgen05.mma
-//   warps 2-5  epilogue (two accumulators: it overlaps the next tile's MMAs)
-// Few tokens and few tiles leave SMs idle, so the K range is split; the last
-// split of a tile to finish (ticket, no spinning) sums the 32-bit partials in
-// split order and runs the epilogue: the same inputs give the same bits.
+//   token rows  up to 16 tokens: bound by the weights' HBM stream and by the
+//               time to its first byte, so weights go from global memory
+//               straight into the fragments of mma.sync, with no descriptor,
+//               barrier or TMEM in front of them.
+//   row tiles   128 weight rows on the MMA's rows (tcgen05), 32 to 128 tokens
+//               on its columns: bound by the weights' stream.
+//   pair tiles  256 tokens x up to 256 weight rows on a CTA pair
+//               (cta_group::2): many tokens, bound by the MMA and by what an
+//               SM can take in from L2 (about 60 bytes a cycle measured,
+//               where a 256 x 256 tile wants 64 to keep its MMA busy).
+//
+// Each splits the K range of a tile over the CTAs of a cluster when the tiles
+// alone leave SMs idle.  The parts of a sum meet in shared memory: each CTA
+// owns a share of the tile's columns, the others write their 32-bit partials
+// of it into the owner's shared memory, and the owner adds them in split
+// order and runs the epilogue.  No partial goes through HBM, nothing spins,
+// and the same inputs give the same bits.
 #include "moe_common.cuh"
 #include "moe_internal.h"
+
+#include <math.h>
 
 namespace moe {
 
@@ -28,261 +36,441 @@ struct LinearArgs {
   const float* bias;
   const void* residual;
   void* out;
-  float* partial;
-  int* tickets;
   int* err;
   int act, residual_f32, out_f32;
   int T, K, N;
   int tiles_n, tiles_t, splits;
-};
-
-template <bool GATED, int BN>
-struct LinearCfg {
-  static constexpr int A_BYTES = (GATED ? 2 : 1) * 128 * 128;
-  static constexpr int B_BYTES = BN * 128;
-  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int STAGES_RAW = 200 * 1024 / STAGE_BYTES;
-  static constexpr int STAGES = STAGES_RAW > 12 ? 12 : STAGES_RAW;
-  static constexpr int ACC_COLS = (GATED ? 2 : 1) * BN;
-  static constexpr int TMEM_COLS = 2 * ACC_COLS < 32 ? 32 : 2 * ACC_COLS;  // powers of two
-  static constexpr int THREADS = 192;
-  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024 + 512;
-  static_assert(TMEM_COLS <= 512 && SMEM_BYTES <= 232448, "budgets");
+  int bn;  // pair tiles: weight rows of a tile
 };
 
 MOE_DEV float silu_f(float v) { return __fdividef(v, 1.f + __expf(-v)); }
+// v * Phi(v), Phi(-|v|) = erfc(|v| / sqrt 2) / 2 by the Chebyshev fit of
+// Numerical Recipes (section 6.2, erfcc: relative error below 1.2e-7
+// everywhere, so the negative tail keeps its precision).
+MOE_DEV float gelu_f(float v) {
+  const float z = fabsf(v) * 0.70710678f;
+  const float t = __fdividef(1.f, fmaf(0.5f, z, 1.f));
+  float p = 0.17087277f;
+  p = fmaf(p, t, -0.82215223f);
+  p = fmaf(p, t, 1.48851587f);
+  p = fmaf(p, t, -1.13520398f);
+  p = fmaf(p, t, 0.27886807f);
+  p = fmaf(p, t, -0.18628806f);
+  p = fmaf(p, t, 0.09678418f);
+  p = fmaf(p, t, 0.37409196f);
+  p = fmaf(p, t, 1.00002368f);
+  p = fmaf(p, t, -1.26551223f);
+  const float tail = 0.5f * t * __expf(fmaf(-z, z, p));
+  return v * (v < 0.f ? tail : 1.f - tail);
+}
 MOE_DEV float activate(int act, float v, float u) {
   if (act == 3) return silu_f(v) * u;
   if (act == 1) return silu_f(v);
-  if (act == 2) return 0.5f * v * erfcf(v * -0.70710678f);  // no 1 + erf near -1
+  if (act == 2) return gelu_f(v);
   return v;
 }
-
-// Outputs of one thread: column n, tokens t0 .. t0 + 15 of which `cols` exist.
-MOE_DEV void write_cols(const LinearArgs& a, int n, int t0, int cols, const float (&v)[16],
-                        const float (&u)[16], float bg, float bu) {
-  if (n >= a.N) return;
-  float r[16];
-  if (a.residual) {
+template <int N>
+MOE_DEV void as_floats(const uint32_t (&r)[N], float (&v)[N]) {
 #pragma unroll
-    for (int c = 0; c < 16; ++c) {
-      const size_t at = static_cast<size_t>(t0 + c) * a.N + n;
-      r[c] = 0.f;
-      if (c < cols)
-        r[c] = a.residual_f32 ? static_cast<const float*>(a.residual)[at]
-                              : __bfloat162float(static_cast<const __nv_bfloat16*>(a.residual)[at]);
+  for (int i = 0; i < N; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// K steps of split s of S.
+MOE_DEV void split_range(int KB, int S, int s, int* kb0, int* kb1) {
+  *kb0 = static_cast<int>(static_cast<long long>(s) * KB / S);
+  *kb1 = static_cast<int>(static_cast<long long>(s + 1) * KB / S);
+}
+
+// ---------------------------------------------------------------------------
+// Token rows: 16 weight rows a CTA (gated: 8 gate rows and the 8 matching up
+// rows, so that a gate and its up sum end in one thread), its 8 warps
+// interleaved along K in pieces of 64.  A lane loads 16 bytes of a weight row
+// and takes its 8 values as the k slots of two m16n8k16 MMAs; the tokens'
+// values are loaded with the same lane-to-k map, so the order of k inside a
+// piece cancels out and both operands are plain 16-byte loads.  One row's
+// piece is a 128-byte line; the next piece's loads are in flight during the
+// MMAs of this one.
+// ---------------------------------------------------------------------------
+constexpr int kTokMaxWarps = 8;
+constexpr int kTokDepth = 4;  // pieces of a warp in flight
+
+MOE_DEV uint4 ldg_stream(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+MOE_DEV void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                       uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+template <int ACT, int NT>  // NT: groups of 8 tokens
+__global__ void __launch_bounds__(32 * kTokMaxWarps, 2)
+    linear_token_kernel(const __nv_bfloat16* __restrict__ x, const __nv_bfloat16* __restrict__ w,
+                        const LinearArgs a) {
+  constexpr bool GATED = ACT == 3;
+  constexpr int COLS = 8 * NT;
+  __shared__ float part[kTokMaxWarps][16][COLS + 1];
+  __shared__ float recv[8][16 * COLS];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warps = blockDim.x >> 5;  // 4 or 8
+  const int S = a.splits;
+  const int s = static_cast<int>(cluster_ctarank());
+  const int n0 = blockIdx.x / S * (GATED ? 8 : 16);
+  if (S > 1) cluster_arrive();
+  grid_dependency_launch();
+  grid_dependency_wait();
+  // weight rows of this lane: fragment rows g and g + 8
+  const int g = lane >> 2, q = lane & 3;
+  const int nlast = a.N - 1;
+  const int row0 = min(n0 + g, nlast);
+  const int row1 = GATED ? a.N + row0 : min(n0 + g + 8, nlast);
+  const __nv_bfloat16* w0 = w + static_cast<size_t>(row0) * a.K + 8 * q;
+  const __nv_bfloat16* w1 = w + static_cast<size_t>(row1) * a.K + 8 * q;
+  int c0, c1;  // pieces of this CTA
+  split_range((a.K + kBK - 1) / kBK, S, s, &c0, &c1);
+
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  float acc[NT][4];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+  // the two halves h of piece c: k = 64 c + 32 h + 8 q
+  uint4 wv[kTokDepth][4];
+  auto load = [&](int c, uint4 (&wr)[4]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int k = c * kBK + 32 * h;
+      const bool in = c < c1 && k + 8 * q < a.K;  // K is a multiple of 8
+      wr[h] = in ? ldg_stream(w0 + k) : zero;
+      wr[2 + h] = in ? ldg_stream(w1 + k) : zero;
+    }
+  };
+#pragma unroll
+  for (int d = 0; d < kTokDepth; ++d) load(c0 + warp + d * warps, wv[d]);
+  for (int c = c0 + warp; c < c1; c += kTokDepth * warps) {
+#pragma unroll
+    for (int d = 0; d < kTokDepth; ++d) {
+      const int cd = c + d * warps;
+      uint4 xv[NT][2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int k = cd * kBK + 32 * h + 8 * q;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const int t = 8 * j + g;
+          xv[j][h] = cd < c1 && k < a.K && t < a.T
+                         ? __ldg(reinterpret_cast<const uint4*>(x + static_cast<size_t>(t) * a.K + k))
+                         : zero;
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          mma_16816(acc[j], wv[d][h].x, wv[d][2 + h].x, wv[d][h].y, wv[d][2 + h].y, xv[j][h].x,
+                    xv[j][h].y);
+          mma_16816(acc[j], wv[d][h].z, wv[d][2 + h].z, wv[d][h].w, wv[d][2 + h].w, xv[j][h].z,
+                    xv[j][h].w);
+        }
+      }
+      load(cd + kTokDepth * warps, wv[d]);
     }
   }
 #pragma unroll
-  for (int c = 0; c < 16; ++c) {
-    if (c < cols) {
-      float o = activate(a.act, v[c] + bg, u[c] + bu);
-      if (a.residual) o += r[c];
-      const size_t at = static_cast<size_t>(t0 + c) * a.N + n;
+  for (int j = 0; j < NT; ++j) {
+    part[warp][g][8 * j + 2 * q] = acc[j][0];
+    part[warp][g][8 * j + 2 * q + 1] = acc[j][1];
+    part[warp][g + 8][8 * j + 2 * q] = acc[j][2];
+    part[warp][g + 8][8 * j + 2 * q + 1] = acc[j][3];
+  }
+  __syncthreads();
+  // sums of the warps (in warp order) to the cluster's first CTA, which adds
+  // them in split order; 16 rows x 8 (4 warps) or 16 tokens a pass
+  if (S > 1) {
+    __syncwarp();
+    cluster_wait();
+    for (int i = threadIdx.x; i < 16 * COLS; i += blockDim.x) {
+      float v = 0.f;
+      for (int k = 0; k < warps; ++k) v += part[k][i & 15][i >> 4];
+      st_cluster_f32(cluster_addr(&recv[s][i], 0), v);
+    }
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+    if (s != 0) return;
+  }
+  for (int i = threadIdx.x; i < 16 * COLS; i += blockDim.x) {
+    const int r = i & 15, t = i >> 4;
+    float v = 0.f;
+    if (S > 1) {
+      for (int k = 0; k < S; ++k) v += recv[k][i];
+    } else {
+      for (int k = 0; k < warps; ++k) v += part[k][r][t];
+    }
+    // gated: rows 8..15 are the up sums of rows 0..7, eight lanes on
+    const float u = GATED ? __shfl_down_sync(0xffffffffu, v, 8) : 0.f;
+    const int n = n0 + r;
+    if (t < a.T && n < a.N && (!GATED || r < 8)) {
+      const size_t at = static_cast<size_t>(t) * a.N + n;
+      float bg = 0.f, bu = 0.f, res = 0.f;
+      if (a.bias) {
+        bg = __ldg(a.bias + n);
+        if constexpr (GATED) bu = __ldg(a.bias + a.N + n);
+      }
+      if (a.residual)
+        res = a.residual_f32
+                  ? static_cast<const float*>(a.residual)[at]
+                  : __bfloat162float(static_cast<const __nv_bfloat16*>(a.residual)[at]);
+      const float o = activate(ACT, v + bg, u + bu) + res;
       if (a.out_f32) static_cast<float*>(a.out)[at] = o;
       else static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(o);
     }
   }
 }
 
-MOE_DEV void load_acc(uint32_t taddr, float (&v)[16]) {
-  uint32_t r[16];
-  tmem_ld16(taddr, r);
-  tmem_ld_wait();
-  reg_fence16(r);
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
+// ---------------------------------------------------------------------------
+// Row tiles: one tile (and K split) per CTA, two CTAs per SM up to
+// 64 tokens.
+// A gated tile takes 64 gate rows and the 64 matching up rows.  Lane = weight
+// row, so the 32 lanes of a warp write 32 neighbouring outputs of one token at
+// any alignment of N.
+//   warp 0     TMA producer      warp 1    TMEM allocation, MMA issue
+//   warps 2-5  epilogue
+// ---------------------------------------------------------------------------
+template <int BN>
+struct RowCfg {
+  static constexpr int A_BYTES = 128 * 128;
+  static constexpr int STAGE_BYTES = A_BYTES + BN * 128;
+  static constexpr int RECV_BYTES = BN * 128 * 4;
+  static constexpr int STAGES = BN == 64 ? 3 : 4;
+  static constexpr int TMEM_COLS = BN;
+  static constexpr int THREADS = 192;
+  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + RECV_BYTES + 1024 + 256;
+  static_assert(SMEM_BYTES <= (BN == 128 ? 232448 : 232448 / 2 - 1024), "shared memory budget");
+};
 
-template <bool GATED, int BN>
-__global__ void __launch_bounds__(LinearCfg<GATED, BN>::THREADS, 1)
-    linear_kernel(const __grid_constant__ CUtensorMap tm_w,
-                  const __grid_constant__ CUtensorMap tm_x, const LinearArgs a) {
-  using C = LinearCfg<GATED, BN>;
+template <int ACT, int BN>
+__global__ void __launch_bounds__(RowCfg<BN>::THREADS)
+    linear_row_kernel(const __grid_constant__ CUtensorMap tm_w,
+                      const __grid_constant__ CUtensorMap tm_x, const LinearArgs a) {
+  using C = RowCfg<BN>;
+  constexpr bool GATED = ACT == 3;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + C::STAGES * C::STAGE_BYTES);
+  float* recv = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE_BYTES);
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(recv + C::RECV_BYTES / 4);
   uint64_t* empty_bar = full_bar + C::STAGES;
-  uint64_t* tfull_bar = empty_bar + C::STAGES;
-  uint64_t* tempty_bar = tfull_bar + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty_bar + 2);
+  uint64_t* done_bar = empty_bar + C::STAGES;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done_bar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  volatile int* last_flag = abort_flag + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int S = a.splits;                               // a power of two, at most BN / 4
+  const int s = static_cast<int>(cluster_ctarank());  // the split of this CTA
+  const int tile = blockIdx.x / S;
+  const int n0 = tile / a.tiles_t * (GATED ? 64 : 128);
+  const int t0 = tile % a.tiles_t * BN;
   const int KB = (a.K + kBK - 1) / kBK;
-  const int units = a.tiles_n * a.tiles_t * a.splits;
+  int kb0, kb1;
+  split_range(KB, S, s, &kb0, &kb1);
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < C::STAGES; ++i) {
-      mbar_init(&full_bar[i], 1);
-      mbar_init(&empty_bar[i], 1);
+  grid_dependency_launch();
+  // one lane: the copies of K step kb into stage st
+  auto load_step = [&](int kb, int st) {
+    uint8_t* sa = smem + st * C::STAGE_BYTES;
+    mbar_arrive_expect_tx(&full_bar[st], C::STAGE_BYTES);
+    tma_load_2d(sa, &tm_w, &full_bar[st], kb * kBK, n0);
+    if constexpr (GATED) tma_load_2d(sa + 64 * 128, &tm_w, &full_bar[st], kb * kBK, a.N + n0);
+    tma_load_2d(sa + C::A_BYTES, &tm_x, &full_bar[st], kb * kBK, t0);
+  };
+  // the first ring of copies is under way before the CTA has set itself up
+  const int ahead = min(C::STAGES, kb1 - kb0);
+  if (warp == 0) {
+    if (elect_one()) {
+      for (int i = 0; i < C::STAGES; ++i) {
+        mbar_init(&full_bar[i], 1);
+        mbar_init(&empty_bar[i], 1);
+      }
+      mbar_init(done_bar, 1);
+      *abort_flag = 0;
+      mbar_fence_init();
+      fence_proxy_async_smem();
+      tma_prefetch_desc(&tm_w);
+      tma_prefetch_desc(&tm_x);
+      grid_dependency_wait();
+      for (int i = 0; i < ahead; ++i) load_step(kb0 + i, i);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&tfull_bar[i], 1);
-      mbar_init(&tempty_bar[i], 4);
-    }
-    *abort_flag = 0;
-    *last_flag = 0;
-    mbar_fence_init();
+    __syncwarp();
+  } else if (warp == 1) {
+    tmem_alloc(tmem_slot, C::TMEM_COLS);
   }
-  if (warp == 1) tmem_alloc(tmem_slot, C::TMEM_COLS);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  cluster_arrive();  // this CTA runs: the others may write into its recv
   const uint32_t tmem_base = *tmem_slot;
 
-  // unit u: split fastest, then the token tiles of one weight tile
-  struct Unit {
-    int tile, n0, t0, s, kb0, kb1;
-  };
-  auto unit_of = [&](int u) {
-    Unit x;
-    x.s = u % a.splits;
-    x.tile = u / a.splits;
-    x.n0 = x.tile / a.tiles_t * 128;
-    x.t0 = x.tile % a.tiles_t * BN;
-    x.kb0 = static_cast<int>(static_cast<long long>(x.s) * KB / a.splits);
-    x.kb1 = static_cast<int>(static_cast<long long>(x.s + 1) * KB / a.splits);
-    return x;
-  };
-
   if (warp == 0) {
-    if (lane == 0) {
-      tma_prefetch_desc(&tm_w);
-      tma_prefetch_desc(&tm_x);
-      uint32_t it = 0;
-      bool alive = true;
-      for (int uu = blockIdx.x; alive && uu < units; uu += gridDim.x) {
-        const Unit u = unit_of(uu);
-        for (int kb = u.kb0; kb < u.kb1; ++kb, ++it) {
-          const int st = it % C::STAGES;
-          if (!mbar_wait(&empty_bar[st], ((it / C::STAGES) & 1u) ^ 1u, abort_flag, a.err)) {
-            alive = false;
-            break;
-          }
-          uint8_t* sa = smem + st * C::STAGE_BYTES;
-          mbar_arrive_expect_tx(&full_bar[st], C::STAGE_BYTES);
-          tma_load_2d(sa, &tm_w, &full_bar[st], kb * kBK, u.n0);
-          if constexpr (GATED)
-            tma_load_2d(sa + 128 * 128, &tm_w, &full_bar[st], kb * kBK, a.N + u.n0);
-          tma_load_2d(sa + C::A_BYTES, &tm_x, &full_bar[st], kb * kBK, u.t0);
-        }
-      }
+    int st = 0;
+    uint32_t ph = 0;
+    for (int kb = kb0 + ahead; kb < kb1; ++kb) {
+      if (!mbar_wait(&empty_bar[st], ph, abort_flag, a.err)) break;
+      if (elect_one()) load_step(kb, st);
+      __syncwarp();
+      if (++st == C::STAGES) st = 0, ph ^= 1;
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      uint32_t it = 0, acc_it = 0;
-      bool alive = true;
-      for (int uu = blockIdx.x; alive && uu < units; uu += gridDim.x, ++acc_it) {
-        const Unit u = unit_of(uu);
-        const int buf = acc_it & 1;
-        if (!mbar_wait(&tempty_bar[buf], ((acc_it >> 1) & 1u) ^ 1u, abort_flag, a.err)) break;
-        tc_fence_after();
-        const uint32_t d = tmem_base + buf * C::ACC_COLS;
-        for (int kb = u.kb0; kb < u.kb1; ++kb, ++it) {
-          const int st = it % C::STAGES;
-          if (!mbar_wait(&full_bar[st], (it / C::STAGES) & 1u, abort_flag, a.err)) {
-            alive = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t sa = smem_u32(smem + st * C::STAGE_BYTES);
-          const uint32_t sb = sa + C::A_BYTES;
-#pragma unroll
-          for (int kk = 0; kk < kBK / 16; ++kk) {
-            const uint32_t acc = (kb > u.kb0 || kk > 0) ? 1u : 0u;
-            const uint64_t bdesc = sw128_desc(sb + kk * 32);
-            umma_f16(d, sw128_desc(sa + kk * 32), bdesc, idesc_bf16_f32(128, BN), acc);
-            if constexpr (GATED)
-              umma_f16(d + BN, sw128_desc(sa + 128 * 128 + kk * 32), bdesc,
-                       idesc_bf16_f32(128, BN), acc);
-          }
-          umma_commit(&empty_bar[st]);
-        }
-        if (!alive) break;
-        umma_commit(&tfull_bar[buf]);
+    const uint64_t desc0 = sw128_desc(smem_u32(smem));
+    bool alive = true;
+    int st = 0;
+    uint32_t ph = 0;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!mbar_wait(&full_bar[st], ph, abort_flag, a.err)) {
+        alive = false;
+        break;
       }
-    }
-  } else {
-    const int ew = warp & 3;  // a warp reads the TMEM lane quarter warp % 4
-    const int row = ew * 32 + lane;
-    uint32_t acc_it = 0;
-    for (int uu = blockIdx.x; uu < units; uu += gridDim.x, ++acc_it) {
-      const Unit u = unit_of(uu);
-      const int buf = acc_it & 1;
-      const bool ok = mbar_wait(&tfull_bar[buf], (acc_it >> 1) & 1u, abort_flag, a.err);
-      if (named_bar_any(1, 128, !ok || *abort_flag)) break;
       tc_fence_after();
-      const uint32_t tb =
-          tmem_base + (static_cast<uint32_t>(ew * 32) << 16) + buf * C::ACC_COLS;
-      const int n = u.n0 + row;
-      const int cols = min(BN, a.T - u.t0);
-      float bg = 0.f, bu = 0.f;
-      if (a.bias && n < a.N) {
-        bg = __ldg(a.bias + n);
-        if constexpr (GATED) bu = __ldg(a.bias + a.N + n);
+      const uint64_t da = desc0 + static_cast<uint64_t>(st * (C::STAGE_BYTES >> 4));
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < kBK / 16; ++kk)
+          umma_f16(tmem_base, da + 2 * kk, da + (C::A_BYTES >> 4) + 2 * kk,
+                   idesc_bf16_f32(128, BN), (kb > kb0 || kk > 0) ? 1u : 0u);
+        umma_commit(&empty_bar[st]);
       }
-      if (a.splits == 1) {
-#pragma unroll 1
-        for (int c0 = 0; c0 < cols; c0 += 16) {
-          float v[16], w[16];
-          load_acc(tb + c0, v);
-          if constexpr (GATED) load_acc(tb + BN + c0, w);
-          write_cols(a, n, u.t0 + c0, cols - c0, v, w, bg, bu);
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&tempty_bar[buf]);
-      } else {
-        // partial [tile][split][column][128 rows]: lanes are neighbours
-        const size_t slot = static_cast<size_t>(C::ACC_COLS) * 128;
-        float* base = a.partial + static_cast<size_t>(u.tile) * a.splits * slot + row;
-        float* mine = base + u.s * slot;
-#pragma unroll 1
-        for (int c0 = 0; c0 < cols; c0 += 16) {
-#pragma unroll
-          for (int h = 0; h < (GATED ? 2 : 1); ++h) {
-            float v[16];
-            load_acc(tb + h * BN + c0, v);
-#pragma unroll
-            for (int c = 0; c < 16; ++c)
-              if (c0 + c < cols) __stcg(mine + static_cast<size_t>(h * BN + c0 + c) * 128, v[c]);
-          }
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&tempty_bar[buf]);
-        named_bar_sync(1, 128);
-        if (threadIdx.x == 64) {
-          const int last = ticket_add_acq_rel(a.tickets + u.tile, 1) == a.splits - 1;
-          if (last) store_relaxed_gpu(a.tickets + u.tile, 0);  // ready for the next launch
-          *last_flag = last;
-        }
-        named_bar_sync(1, 128);
-        if (*last_flag) {
-#pragma unroll 1
-          for (int c0 = 0; c0 < cols; c0 += 16) {
-            float v[16], w[16];
-#pragma unroll
-            for (int c = 0; c < 16; ++c) v[c] = w[c] = 0.f;
-            for (int s = 0; s < a.splits; ++s) {
-              const float* p = base + s * slot;
-#pragma unroll
-              for (int c = 0; c < 16; ++c)
-                if (c0 + c < cols) {
-                  v[c] += __ldcg(p + static_cast<size_t>(c0 + c) * 128);
-                  if constexpr (GATED) w[c] += __ldcg(p + static_cast<size_t>(BN + c0 + c) * 128);
-                }
-            }
-            write_cols(a, n, u.t0 + c0, cols - c0, v, w, bg, bu);
-          }
-        }
-      }
+      __syncwarp();
+      if (++st == C::STAGES) st = 0, ph ^= 1;
     }
+    if (alive && elect_one()) umma_commit(done_bar);
+    __syncwarp();
   }
 
+  // this CTA's partial sums into the owners' shared memory: owner q has the
+  // token columns [q * P, (q + 1) * P), as recv[split][P / 4][128 rows][4]: a
+  // warp's 16-byte stores to another SM are 512 contiguous bytes (scattered
+  // 16-byte rows took twice the time of 4-byte stores, these a third)
+  const int P = BN / S;
+  const int lp = __ffs(P) - 1;
+  const int cols = min(BN, a.T - t0);
+  const int mine = min(P, cols - s * P);  // token columns that this CTA owns
+  const int ew = warp & 3;                // a warp reads the TMEM lane quarter warp % 4
+  const int row = ew * 32 + lane;
+  // thread -> output column and first token of the epilogue: gated tiles have
+  // 64 columns, and their two halves of the threads take tokens in turn
+  const int r = GATED ? (row & 63) : row;
+  const int n = n0 + r;
+  constexpr int U = 4;                       // tokens of a 16-byte read
+  constexpr int STEP = GATED ? 2 * U : U;
+  const int first = GATED ? (row >> 6) * U : 0;
+  constexpr int KEEP = 8;                    // reads whose residual is fetched ahead
+  float res[KEEP][U];
+  auto load_residual = [&](int p0, float (&v)[U]) {
+    const size_t at = static_cast<size_t>(t0 + s * P + p0) * a.N + n;
+    if (a.residual_f32) {
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+        v[i] = p0 + i < mine ? static_cast<const float*>(a.residual)[at + static_cast<size_t>(i) * a.N] : 0.f;
+    } else {
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+        v[i] = p0 + i < mine ? __bfloat162float(static_cast<const __nv_bfloat16*>(
+                                   a.residual)[at + static_cast<size_t>(i) * a.N])
+                             : 0.f;
+    }
+  };
+  bool ok = true;
+  if (warp >= 2) {
+    grid_dependency_wait();
+#pragma unroll
+    for (int k = 0; k < KEEP; ++k)
+#pragma unroll
+      for (int i = 0; i < U; ++i) res[k][i] = 0.f;
+    if (a.residual && n < a.N) {
+#pragma unroll
+      for (int k = 0; k < KEEP; ++k) load_residual(first + k * STEP, res[k]);
+    }
+    ok = mbar_wait(done_bar, 0, abort_flag, a.err);
+    tc_fence_after();
+  }
+  __syncwarp();
+  cluster_wait();
+  if (warp >= 2) {
+    if (ok) {
+      const float* to = recv + s * P * 128 + row * 4;
+#pragma unroll 1
+      for (int c0 = 0; c0 < cols; c0 += 16) {
+        uint32_t v[16];
+        tmem_ld16(tmem_base + (static_cast<uint32_t>(ew * 32) << 16) + c0, v);
+        tmem_ld_wait();
+        reg_fence16(v);
+#pragma unroll
+        for (int c = 0; c < 16; c += U) {
+          const int q = (c0 + c) >> lp;  // P >= 4 and a power of two
+          if (c0 + c < cols)
+            st_cluster_v4(cluster_addr(to + ((c0 + c) & (P - 1)) * 128, q), v[c], v[c + 1], v[c + 2],
+                          v[c + 3]);
+        }
+      }
+    }
+    tc_fence_before();
+  }
+  __syncwarp();
+  cluster_sync_all();
+
+  if (warp >= 2 && n < a.N) {
+    float bg = 0.f, bu = 0.f;
+    if (a.bias) {
+      bg = __ldg(a.bias + n);
+      if constexpr (GATED) bu = __ldg(a.bias + a.N + n);
+    }
+    auto finish = [&](int p0, const float (&rs)[U]) {
+      float v[U], u[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i) v[i] = u[i] = 0.f;
+      for (int q = 0; q < S; ++q) {
+        const float* from = recv + (q * P + p0) * 128 + r * 4;
+        const float4 f = *reinterpret_cast<const float4*>(from);
+        v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
+        if constexpr (GATED) {
+          const float4 h = *reinterpret_cast<const float4*>(from + 64 * 4);
+          u[0] += h.x, u[1] += h.y, u[2] += h.z, u[3] += h.w;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < U; ++i) v[i] = activate(ACT, v[i] + bg, u[i] + bu) + rs[i];
+      const size_t at = static_cast<size_t>(t0 + s * P + p0) * a.N + n;
+      if (a.out_f32) {
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+          if (p0 + i < mine) static_cast<float*>(a.out)[at + static_cast<size_t>(i) * a.N] = v[i];
+      } else {
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+          if (p0 + i < mine)
+            static_cast<__nv_bfloat16*>(a.out)[at + static_cast<size_t>(i) * a.N] =
+                __float2bfloat16_rn(v[i]);
+      }
+    };
+#pragma unroll
+    for (int k = 0; k < KEEP; ++k)
+      if (first + k * STEP < mine) finish(first + k * STEP, res[k]);
+    for (int p0 = first + KEEP * STEP; p0 < mine; p0 += KEEP * STEP) {
+      if (a.residual) {
+#pragma unroll
+        for (int k = 0; k < KEEP; ++k) load_residual(p0 + k * STEP, res[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < KEEP; ++k)
+        if (p0 + k * STEP < mine) finish(p0 + k * STEP, res[k]);
+    }
+  }
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
@@ -290,59 +478,588 @@ __global__ void __launch_bounds__(LinearCfg<GATED, BN>::THREADS, 1)
   }
 }
 
-template <bool GATED, int BN>
-int launch_tile(const CUtensorMap& tw, const CUtensorMap& tx, const LinearArgs& a, int num_sms,
-                cudaStream_t stream) {
-  using C = LinearCfg<GATED, BN>;
-  static std::atomic<unsigned long long> smem_set{0};
-  if (!ensure_smem_limit(reinterpret_cast<const void*>(linear_kernel<GATED, BN>), C::SMEM_BYTES,
-                         smem_set))
-    return -1;
-  const int units = a.tiles_n * a.tiles_t * a.splits;
-  const int grid = units < num_sms ? units : num_sms;
-  linear_kernel<GATED, BN><<<grid, C::THREADS, C::SMEM_BYTES, stream>>>(tw, tx, a);
+// ---------------------------------------------------------------------------
+// Pair tiles: 256 tokens x bn weight rows on a CTA pair.  Each CTA holds 128
+// of the tokens and half of the weight rows (gated: one CTA the gate rows,
+// the other the matching up rows); lane = token, so a gated output's gate and
+// up columns c and c + bn/2 lie in one thread.  The even CTA's warp issues
+// the pair's MMAs and every copy counts on its barrier.
+//   SPLIT = false: persistent pairs, two TMEM accumulators, so the epilogue of
+//                  one tile overlaps the MMAs of the next
+//   SPLIT = true:  one tile per cluster of `splits` pairs, each a part of K;
+//                  the ring is the receive buffer once its MMAs are done
+//   warp 0     TMA producer      warp 1    TMEM allocation, MMA issue
+//   warps 2-9  epilogue, two per TMEM lane quarter
+// ---------------------------------------------------------------------------
+constexpr int kPairStages = 6;
+constexpr int kPairStageBytes = 2 * 128 * 128;
+constexpr int kPairEpiWarps = 8;
+constexpr int kPairThreads = 64 + 32 * kPairEpiWarps;
+constexpr int kPairPitch = 17;  // floats of a staged row of 16 columns
+constexpr int kPairStagedBytes = kPairEpiWarps * 32 * kPairPitch * 4;
+constexpr int kPairSmem = kPairStages * kPairStageBytes + 1024 + 512 + kPairStagedBytes;
+static_assert(kPairSmem <= 232448, "shared memory budget");
+
+// A chunk is 16 output columns n .. n + 15 (n < N) of the 32 tokens trow0 ..
+// trow0 + 31.  VEC (N % 16 == 0, 32-byte bases): a lane has one token and moves
+// its 16 values as vectors.  Otherwise, rows of N elements at any alignment:
+// the chunk is turned in shared memory so that neighbouring lanes touch
+// neighbouring columns; lane -> column lane % 16 of tokens lane / 16 + 2 j.
+template <bool VEC>
+MOE_DEV void chunk_residual(const LinearArgs& a, int trow0, int n, uint32_t (&raw)[16]) {
+  const int lane = threadIdx.x & 31;
+  if constexpr (VEC) {
+    const int t = trow0 + lane;
+    if (t < a.T) {
+      const size_t at = static_cast<size_t>(t) * a.N + n;
+      const uint4* p = a.residual_f32
+                           ? reinterpret_cast<const uint4*>(static_cast<const float*>(a.residual) + at)
+                           : reinterpret_cast<const uint4*>(
+                                 static_cast<const __nv_bfloat16*>(a.residual) + at);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i < 2 || a.residual_f32) {
+          const uint4 v = p[i];
+          raw[4 * i] = v.x, raw[4 * i + 1] = v.y, raw[4 * i + 2] = v.z, raw[4 * i + 3] = v.w;
+        }
+      }
+    }
+  } else {
+    const int c = lane & 15, tq = trow0 + (lane >> 4);
+    const size_t p0 = static_cast<size_t>(tq) * a.N + n + c;
+    const int rows = n + c < a.N ? a.T - tq : 0;
+    if (a.residual_f32) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (2 * j < rows)
+          raw[j] = __float_as_uint(
+              static_cast<const float*>(a.residual)[p0 + static_cast<size_t>(2 * j) * a.N]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (2 * j < rows)
+          raw[j] = static_cast<uint32_t>(static_cast<const uint16_t*>(
+                       a.residual)[p0 + static_cast<size_t>(2 * j) * a.N])
+                   << 16;
+    }
+  }
+}
+
+template <int ACT, bool VEC>
+MOE_DEV void chunk_finish(const LinearArgs& a, int trow0, int n, float* staged, float (&v)[16],
+                          float (&u)[16], const uint32_t (&raw)[16]) {
+  constexpr bool GATED = ACT == 3;
+  const int lane = threadIdx.x & 31;
+  if (a.bias) {
+#pragma unroll
+    for (int c = 0; c < 16; ++c)
+      if (VEC || n + c < a.N) {
+        v[c] += __ldg(a.bias + n + c);
+        if constexpr (GATED) u[c] += __ldg(a.bias + a.N + n + c);
+      }
+  }
+#pragma unroll
+  for (int c = 0; c < 16; ++c) v[c] = activate(ACT, v[c], GATED ? u[c] : 0.f);
+  if constexpr (VEC) {
+    const int t = trow0 + lane;
+    if (t >= a.T) return;
+    const size_t at = static_cast<size_t>(t) * a.N + n;
+    if (a.residual) {
+      if (a.residual_f32) {
+#pragma unroll
+        for (int c = 0; c < 16; ++c) v[c] += __uint_as_float(raw[c]);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          v[2 * c] += __uint_as_float(raw[c] << 16);
+          v[2 * c + 1] += __uint_as_float(raw[c] & 0xFFFF0000u);
+        }
+      }
+    }
+    if (a.out_f32) {
+      float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.out) + at);
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        o[c] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+    } else {
+      uint32_t o[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) o[c] = pack_bf16x2(v[2 * c], v[2 * c + 1]);
+      st_global_v8(static_cast<__nv_bfloat16*>(a.out) + at, o);
+    }
+  } else {
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < 16; ++c) staged[lane * kPairPitch + c] = v[c];
+    __syncwarp();
+    const int c = lane & 15, tq = trow0 + (lane >> 4);
+    const size_t p0 = static_cast<size_t>(tq) * a.N + n + c;
+    const int rows = n + c < a.N ? a.T - tq : 0;
+    const float* from = staged + (lane >> 4) * kPairPitch + c;
+    float o[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) o[j] = from[2 * j * kPairPitch];
+    if (a.residual) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) o[j] += __uint_as_float(raw[j]);
+    }
+    if (a.out_f32) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (2 * j < rows)
+          static_cast<float*>(a.out)[p0 + static_cast<size_t>(2 * j) * a.N] = o[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (2 * j < rows)
+          static_cast<__nv_bfloat16*>(a.out)[p0 + static_cast<size_t>(2 * j) * a.N] =
+              __float2bfloat16_rn(o[j]);
+    }
+  }
+}
+
+// The chunks first, first + 2, ... below end of one tile by one warp, the next
+// chunk's residual in flight while one is computed; fetch(j, v, u) gives the
+// sums of chunk j.  raw holds the first chunk's residual.
+template <int ACT, bool VEC, class Fetch>
+MOE_DEV void chunk_loop(const LinearArgs& a, int trow0, int n0, int first, int end, float* staged,
+                        uint32_t (&raw)[16], Fetch&& fetch) {
+#pragma unroll 1
+  for (int j = first; j < end; j += 2) {
+    uint32_t next[16];
+    if (a.residual && j + 2 < end) chunk_residual<VEC>(a, trow0, n0 + 16 * (j + 2), next);
+    float v[16], u[16];
+    fetch(j, v, u);
+    chunk_finish<ACT, VEC>(a, trow0, n0 + 16 * j, staged, v, u, raw);
+#pragma unroll
+    for (int c = 0; c < 16; ++c) raw[c] = next[c];
+  }
+}
+
+template <int ACT, bool VEC, bool SPLIT>
+__global__ void __launch_bounds__(kPairThreads, 1)
+    linear_pair_kernel(const __grid_constant__ CUtensorMap tm_w,
+                       const __grid_constant__ CUtensorMap tm_x, const LinearArgs a) {
+  constexpr bool GATED = ACT == 3;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + kPairStages * kPairStageBytes);
+  uint64_t* empty_bar = full_bar + kPairStages;
+  uint64_t* tfull_bar = empty_bar + kPairStages;
+  uint64_t* tempty_bar = tfull_bar + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty_bar + 2);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  float* staged = reinterpret_cast<float*>(smem + kPairStages * kPairStageBytes + 512);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t crank = cluster_ctarank();
+  const int rank = static_cast<int>(crank & 1u);       // place in the pair
+  const uint32_t leader = crank & ~1u;                 // cluster rank of the pair's even CTA
+  const int pr = static_cast<int>(crank >> 1);         // the pair's split of K
+  const uint16_t pair_mask = static_cast<uint16_t>(3u << leader);
+  const int S = SPLIT ? a.splits : 1;
+  const int cid = blockIdx.x / (2 * S);
+  const int ncl = gridDim.x / (2 * S);
+  const int KB = (a.K + kBK - 1) / kBK;
+  int kb0 = 0, kb1 = KB;
+  if constexpr (SPLIT) split_range(KB, S, pr, &kb0, &kb1);
+  const int tiles = a.tiles_t * a.tiles_n;
+  const int half = a.bn >> 1;                 // weight rows of a CTA
+  const int out_cols = GATED ? half : a.bn;   // output columns of a tile
+
+  if (threadIdx.x == 0) {
+    tma_prefetch_desc(&tm_w);
+    tma_prefetch_desc(&tm_x);
+    for (int i = 0; i < kPairStages; ++i) {
+      mbar_init(&full_bar[i], 1);
+      mbar_init(&empty_bar[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&tfull_bar[i], 1);
+      mbar_init(&tempty_bar[i], 2 * kPairEpiWarps);
+    }
+    *abort_flag = 0;
+    mbar_fence_init();
+  }
+  if (warp == 1) tmem_alloc_pair(tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // both CTAs' barriers exist before a copy or commit reaches them
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  grid_dependency_launch();
+  grid_dependency_wait();
+
+  // tile order: groups of 8 token tiles, walked token-tile-fastest, so the
+  // pairs running at one time share a compact block of x and w in L2
+  struct Tile {
+    int t0, n0;
+  };
+  auto tile_of = [&](int i) {
+    const int per = 8 * a.tiles_n;
+    const int g = i / per, r = i % per;
+    const int gm = min(8, a.tiles_t - g * 8);
+    Tile x;
+    x.t0 = (g * 8 + r % gm) * 256;
+    x.n0 = r / gm * out_cols;
+    return x;
+  };
+
+  if (warp == 0) {
+    const uint32_t bytes = 2 * (128 + half) * 128;  // both CTAs' copies of a step
+    const uint32_t bar0 = cluster_addr(full_bar, leader);
+    bool alive = true;
+    int st = 0;
+    uint32_t ph = 1;
+    for (int i = cid; alive && i < tiles; i += ncl) {
+      const Tile tl = tile_of(i);
+      const int trow = tl.t0 + rank * 128;
+      const int wrow = tl.n0 + rank * (GATED ? a.N : half);
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!mbar_wait(&empty_bar[st], ph, abort_flag, a.err)) {
+          alive = false;
+          break;
+        }
+        if (elect_one()) {
+          if (rank == 0) mbar_arrive_expect_tx(&full_bar[st], bytes);
+          uint8_t* sa = smem + st * kPairStageBytes;
+          tma_load_2d_pair(sa, &tm_x, bar0 + 8 * st, kb * kBK, trow);
+          tma_load_2d_pair(sa + 128 * 128, &tm_w, bar0 + 8 * st, kb * kBK, wrow);
+        }
+        __syncwarp();
+        if (++st == kPairStages) st = 0, ph ^= 1;
+      }
+    }
+  } else if (warp == 1) {
+    if (rank == 0) {
+      const uint32_t idesc = idesc_bf16_f32(256, 0) | (static_cast<uint32_t>(a.bn >> 3) << 17);
+      const uint64_t desc0 = sw128_desc(smem_u32(smem));
+      bool alive = true;
+      int st = 0;
+      uint32_t ph = 0, acc_it = 0;
+      for (int i = cid; alive && i < tiles; i += ncl, ++acc_it) {
+        const int buf = acc_it & 1;
+        if (!mbar_wait(&tempty_bar[buf], ((acc_it >> 1) & 1u) ^ 1u, abort_flag, a.err)) break;
+        tc_fence_after();
+        const uint32_t d = tmem_base + buf * 256;
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!mbar_wait(&full_bar[st], ph, abort_flag, a.err)) {
+            alive = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t da = desc0 + static_cast<uint64_t>(st * (kPairStageBytes >> 4));
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < kBK / 16; ++kk)
+              umma_f16_pair(d, da + 2 * kk, da + (128 * 128 >> 4) + 2 * kk, idesc,
+                            (kb > kb0 || kk > 0) ? 1u : 0u);
+            umma_commit_pair(&empty_bar[st], pair_mask);
+          }
+          __syncwarp();
+          if (++st == kPairStages) st = 0, ph ^= 1;
+        }
+        if (alive && elect_one()) umma_commit_pair(&tfull_bar[buf], pair_mask);
+        __syncwarp();
+      }
+    }
+  } else if constexpr (!SPLIT) {
+    const int ew = warp & 3;           // TMEM lane quarter of this warp
+    const int ch = (warp - 2) >> 2;    // it takes every other chunk of 16 columns
+    float* st = staged + (warp - 2) * 32 * kPairPitch;
+    uint32_t acc_it = 0;
+    for (int i = cid; i < tiles; i += ncl, ++acc_it) {
+      const Tile tl = tile_of(i);
+      const int buf = acc_it & 1;
+      const int trow0 = tl.t0 + rank * 128 + ew * 32;  // token of lane 0
+      const int chunks = (min(out_cols, a.N - tl.n0) + 15) / 16;
+      uint32_t raw[16];
+      if (a.residual && ch < chunks) chunk_residual<VEC>(a, trow0, tl.n0 + 16 * ch, raw);
+      const bool ok = mbar_wait(&tfull_bar[buf], (acc_it >> 1) & 1u, abort_flag, a.err);
+      if (named_bar_any(1, 32 * kPairEpiWarps, !ok || *abort_flag)) break;
+      tc_fence_after();
+      const uint32_t tb = tmem_base + (static_cast<uint32_t>(ew * 32) << 16) + buf * 256;
+      chunk_loop<ACT, VEC>(a, trow0, tl.n0, ch, chunks, st, raw,
+                           [&](int j, float (&v)[16], float (&u)[16]) {
+        uint32_t x[16], y[16];
+        tmem_ld16(tb + 16 * j, x);
+        if constexpr (GATED) tmem_ld16(tb + half + 16 * j, y);
+        tmem_ld_wait();
+        reg_fence16(x);
+        as_floats(x, v);
+        if constexpr (GATED) {
+          reg_fence16(y);
+          as_floats(y, u);
+        }
+      });
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(cluster_addr(&tempty_bar[buf], leader));
+    }
+  }
+
+  if constexpr (SPLIT) {
+    const Tile tl = tile_of(cid);
+    const int ew = warp & 3, ch = (warp - 2) >> 2;
+    const int row = ew * 32 + lane;
+    const uint32_t tb = tmem_base + (static_cast<uint32_t>(ew * 32) << 16);
+    const int cols = min(out_cols, a.N - tl.n0);
+    // owner q has the chunks [q * own, (q + 1) * own) of 16 output columns, as
+    // recv[other split][own chunk][gate, up: 16 / 4][128 rows][4] (see the row tiles)
+    constexpr int W = GATED ? 32 : 16;  // sums of a chunk and row
+    const int chunks = (cols + 15) / 16;
+    const int own = (out_cols / 16 + S - 1) / S;
+    const int trow0 = tl.t0 + rank * 128 + ew * 32;
+    const int end = min(chunks, (pr + 1) * own);
+    float* recv = reinterpret_cast<float*>(smem);
+    uint32_t raw[16];
+    bool ok = true;
+    if (warp >= 2) {
+      if (a.residual && pr * own + ch < end)
+        chunk_residual<VEC>(a, trow0, tl.n0 + 16 * (pr * own + ch), raw);
+      ok = mbar_wait(&tfull_bar[0], 0, abort_flag, a.err);
+      tc_fence_after();
+    }
+    __syncwarp();
+    cluster_sync_all();  // every ring of the cluster is done with
+    if (warp >= 2 && ok) {
+#pragma unroll 1
+      for (int j = ch; j < chunks; j += 2) {
+        const int q = j / own;
+        if (q == pr) continue;
+        const int from = pr < q ? pr : pr - 1;  // this split's slot at owner q
+        const uint32_t dst =
+            cluster_addr(recv + ((from * own + j - q * own) * W * 128 + row * 4), 2 * q + rank);
+        uint32_t x[16], y[16];
+        tmem_ld16(tb + 16 * j, x);
+        if constexpr (GATED) tmem_ld16(tb + half + 16 * j, y);
+        tmem_ld_wait();
+        reg_fence16(x);
+#pragma unroll
+        for (int c = 0; c < 16; c += 4)
+          st_cluster_v4(dst + 512 * c, x[c], x[c + 1], x[c + 2], x[c + 3]);
+        if constexpr (GATED) {
+          reg_fence16(y);
+#pragma unroll
+          for (int c = 0; c < 16; c += 4)
+            st_cluster_v4(dst + 512 * (16 + c), y[c], y[c + 1], y[c + 2], y[c + 3]);
+        }
+      }
+    }
+    __syncwarp();
+    cluster_sync_all();
+    if (warp >= 2 && ok) {
+      chunk_loop<ACT, VEC>(a, trow0, tl.n0, pr * own + ch, end,
+                           staged + (warp - 2) * 32 * kPairPitch, raw,
+                           [&](int j, float (&v)[16], float (&u)[16]) {
+        uint32_t x[16], y[16];
+        tmem_ld16(tb + 16 * j, x);
+        if constexpr (GATED) tmem_ld16(tb + half + 16 * j, y);
+        tmem_ld_wait();
+        reg_fence16(x);
+        if constexpr (GATED) reg_fence16(y);
+#pragma unroll
+        for (int c = 0; c < 16; ++c) v[c] = u[c] = 0.f;
+        for (int q = 0; q < S; ++q) {  // in split order
+          if (q == pr) {
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              v[c] += __uint_as_float(x[c]);
+              if constexpr (GATED) u[c] += __uint_as_float(y[c]);
+            }
+          } else {
+            const float4* p = reinterpret_cast<const float4*>(
+                recv + ((q < pr ? q : q - 1) * own + j - pr * own) * W * 128 + row * 4);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const float4 f = p[c * 128];
+              v[4 * c] += f.x, v[4 * c + 1] += f.y, v[4 * c + 2] += f.z, v[4 * c + 3] += f.w;
+            }
+            if constexpr (GATED) {
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const float4 f = p[(4 + c) * 128];
+                u[4 * c] += f.x, u[4 * c + 1] += f.y, u[4 * c + 2] += f.z, u[4 * c + 3] += f.w;
+              }
+            }
+          }
+        }
+      });
+      tc_fence_before();
+    }
+  }
+
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, 512);
+  }
+  // neither CTA leaves while the other may still copy, commit or arrive here
+  cluster_sync_all();
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+// Cluster launch that may start before the kernel in front of it has ended.
+template <class Kernel, class... Args>
+int launch_cluster(Kernel kernel, int cluster, int grid, int threads, int smem,
+                   cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) return -1;
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
+}
+
+template <int ACT, int NT>
+int launch_token(const void* x, const void* w, const LinearArgs& a, cudaStream_t stream) {
+  return launch_cluster(linear_token_kernel<ACT, NT>, a.splits, a.tiles_n * a.splits, 32 * a.bn, 0,
+                        stream, static_cast<const __nv_bfloat16*>(x),
+                        static_cast<const __nv_bfloat16*>(w), a);
+}
+template <int NT>
+int launch_token_act(int act, const void* x, const void* w, const LinearArgs& a,
+                     cudaStream_t stream) {
+  return act == 0   ? launch_token<0, NT>(x, w, a, stream)
+         : act == 1 ? launch_token<1, NT>(x, w, a, stream)
+         : act == 2 ? launch_token<2, NT>(x, w, a, stream)
+                    : launch_token<3, NT>(x, w, a, stream);
+}
+
+template <int ACT, int BN>
+int launch_row(const CUtensorMap& tw, const CUtensorMap& tx, const LinearArgs& a,
+               cudaStream_t stream) {
+  using C = RowCfg<BN>;
+  static std::atomic<unsigned long long> smem_set{0};
+  const auto kernel = linear_row_kernel<ACT, BN>;
+  if (!ensure_smem_limit(reinterpret_cast<const void*>(kernel), C::SMEM_BYTES, smem_set)) return -1;
+  return launch_cluster(kernel, a.splits, a.tiles_n * a.tiles_t * a.splits, C::THREADS,
+                        C::SMEM_BYTES, stream, tw, tx, a);
+}
+
+template <int BN>
+int launch_row_act(int act, const CUtensorMap& tw, const CUtensorMap& tx, const LinearArgs& a,
+                   cudaStream_t stream) {
+  return act == 0   ? launch_row<0, BN>(tw, tx, a, stream)
+         : act == 1 ? launch_row<1, BN>(tw, tx, a, stream)
+         : act == 2 ? launch_row<2, BN>(tw, tx, a, stream)
+                    : launch_row<3, BN>(tw, tx, a, stream);
+}
+
+template <int ACT, bool VEC>
+int launch_pair(const CUtensorMap& tw, const CUtensorMap& tx, const LinearArgs& a, int num_sms,
+                cudaStream_t stream) {
+  static std::atomic<unsigned long long> split_set{0}, whole_set{0};
+  const int tiles = a.tiles_n * a.tiles_t;
+  if (a.splits > 1) {
+    const auto kernel = linear_pair_kernel<ACT, VEC, true>;
+    if (!ensure_smem_limit(reinterpret_cast<const void*>(kernel), kPairSmem, split_set)) return -1;
+    return launch_cluster(kernel, 2 * a.splits, 2 * a.splits * tiles, kPairThreads, kPairSmem,
+                          stream, tw, tx, a);
+  }
+  const auto kernel = linear_pair_kernel<ACT, VEC, false>;
+  if (!ensure_smem_limit(reinterpret_cast<const void*>(kernel), kPairSmem, whole_set)) return -1;
+  const int pairs = tiles < num_sms / 2 ? tiles : num_sms / 2;
+  return launch_cluster(kernel, 2, 2 * pairs, kPairThreads, kPairSmem, stream, tw, tx, a);
+}
+template <bool VEC>
+int launch_pair_act(int act, const CUtensorMap& tw, const CUtensorMap& tx, const LinearArgs& a,
+                    int num_sms, cudaStream_t stream) {
+  return act == 0   ? launch_pair<0, VEC>(tw, tx, a, num_sms, stream)
+         : act == 1 ? launch_pair<1, VEC>(tw, tx, a, num_sms, stream)
+         : act == 2 ? launch_pair<2, VEC>(tw, tx, a, num_sms, stream)
+                    : launch_pair<3, VEC>(tw, tx, a, num_sms, stream);
 }
 
 }  // namespace
 
+// Estimated cycles of every tiling, and the cheapest.  Measured on GB300: an
+// SM takes in about 57 bytes a cycle from L2, a ring turns over in about 2300
+// cycles when it streams from HBM, a K step costs its issuing warp about 380
+// cycles and a pair's MMA 2 bn; clusters of 2, 4, 6, 8 CTAs with a pair
+// tile's shared memory fit 76, 36, 23, 15 times on 152 SMs.  What a launch
+// costs before its first and after its last K step: row tiles about 6000
+// cycles and 1500 more when split, pair tiles 7000 and 4000 more.
 LinearPlan plan_linear(int T, int K, int N, bool gated, int num_sms) {
-  LinearPlan p{};
-  p.bn = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
-  p.tiles_n = (N + 127) / 128;
-  p.tiles_t = (T + p.bn - 1) / p.bn;
+  LinearPlan best{};
   const int KB = (K + kBK - 1) / kBK;
-  const long long tiles = static_cast<long long>(p.tiles_n) * p.tiles_t;
-  p.splits = 1;
-  if (tiles > 0 && tiles < num_sms) {
-    int s = static_cast<int>(num_sms / tiles);
-    if (s > KB / 4) s = KB / 4;  // at least four K steps a unit
-    if (s > 1) p.splits = s;
+  if (T <= 16) {
+    // a CTA has 4 or 8 pieces in flight a warp; K is split only when there are
+    // fewer tiles than SMs
+    best.kind = kLinearToken;
+    best.tiles_n = (N + (gated ? 7 : 15)) / (gated ? 8 : 16);
+    best.tiles_t = 1;
+    best.splits = 1;
+    while (best.splits < 8 && best.tiles_n * best.splits < num_sms && KB / (2 * best.splits) >= 8)
+      best.splits *= 2;
+    best.bn = KB / best.splits >= 64 ? 8 : 4;
+    return best;
   }
-  p.partial_bytes = p.splits > 1 ? align_up(static_cast<size_t>(tiles) * p.splits *
-                                                (gated ? 2 : 1) * p.bn * 128 * 4,
-                                            256)
-                                 : 0;
-  return p;
+  const double ingest = 57.0, turn = 2300.0, issue = 380.0;
+  // the operands' HBM time, which no tiling beats (6.7 TB/s at 1.9 GHz)
+  const double hbm = (2.0 * T * K + 2.0 * K * N * (gated ? 2 : 1)) / 3520.0;
+  double least = 1e30;
+  auto consider = [&](LinearKind kind, int bn, int s, int tiles_n, int tiles_t, double cycles) {
+    if (cycles < least) {
+      least = cycles;
+      best.kind = kind;
+      best.bn = bn;
+      best.splits = s;
+      best.tiles_n = tiles_n;
+      best.tiles_t = tiles_t;
+    }
+  };
+  for (int bn = 32; bn <= 128; bn *= 2) {
+    // the smallest tile that holds all tokens, or tiles of 64 or 128
+    if (T <= 128 ? (bn < T || bn >= 2 * T) && !(bn == 32 && T < 32) : bn < 64 || T > 1024) continue;
+    const int tn = (N + (gated ? 63 : 127)) / (gated ? 64 : 128), tt = (T + bn - 1) / bn;
+    const double stage = 16384 + 128.0 * bn;
+    const int ring = bn == 64 ? 3 : 4, fit = bn == 128 ? num_sms : 2 * num_sms;
+    for (int s = 1; s <= 8 && s <= KB; s *= 2) {
+      const double units = static_cast<double>(tn) * tt * s;
+      const double share = bn == 128 || units <= num_sms ? 1.0 : 2.0;  // CTAs of an SM
+      const double step = fmax(fmax(stage * share / ingest, turn / ring), issue);
+      const double run = ceil(units / fit) * ((KB + s - 1) / s) * step;
+      consider(kLinearRow, bn, s, tn, tt, fmax(run, hbm) + 6000 + (s > 1 ? 1500 : 0) + 8.0 * bn);
+    }
+  }
+  if (T > 64) {
+    for (int bn = 64; bn <= 256; bn += 32) {
+      const int oc = gated ? bn / 2 : bn;
+      const int tn = (N + oc - 1) / oc, tt = (T + 255) / 256;
+      const double step = fmax(fmax((16384 + 64.0 * bn) / ingest, issue), 2.0 * bn);
+      for (int s = 1; s <= 4 && s <= KB; ++s) {
+        const int fit = s == 1 ? num_sms / 2 : num_sms * (s == 2 ? 36 : s == 3 ? 23 : 15) / 152;
+        const double waves = ceil(static_cast<double>(tn) * tt / (fit > 0 ? fit : 1));
+        const double run = waves * (((KB + s - 1) / s) * step + (s > 1 ? 4000 : 0));
+        consider(kLinearPair, bn, s, tn, tt, fmax(run, hbm) + 7000 + 10.0 * bn);
+      }
+    }
+  }
+  return best;
 }
 
 int launch_linear(const void* x, const void* w, const float* bias, int act, const void* residual,
                   int residual_f32, int T, int K, int N, void* out, int out_f32,
-                  const LinearPlan& plan, float* partial, int* tickets, int* err, int num_sms,
-                  cudaStream_t stream, const char** why) {
-  const bool gated = act == 3;
-  CUtensorMap tw, tx;
-  if (!make_map_bf16(&tw, w, static_cast<uint64_t>(N) * (gated ? 2 : 1), K, 128) ||
-      !make_map_bf16(&tx, x, T, K, plan.bn)) {
-    *why = "cuTensorMapEncodeTiled failed for the dense product";
-    return -1;
-  }
+                  const LinearPlan& plan, int* err, int num_sms, cudaStream_t stream,
+                  const char** why) {
   LinearArgs a{};
   a.bias = bias;
   a.residual = residual;
   a.out = out;
-  a.partial = partial;
-  a.tickets = tickets;
   a.err = err;
   a.act = act;
   a.residual_f32 = residual_f32;
@@ -353,17 +1070,30 @@ int launch_linear(const void* x, const void* w, const float* bias, int act, cons
   a.tiles_n = plan.tiles_n;
   a.tiles_t = plan.tiles_t;
   a.splits = plan.splits;
+  a.bn = plan.bn;
   int rc;
-  if (gated) {
-    rc = plan.bn == 16   ? launch_tile<true, 16>(tw, tx, a, num_sms, stream)
-         : plan.bn == 32 ? launch_tile<true, 32>(tw, tx, a, num_sms, stream)
-         : plan.bn == 64 ? launch_tile<true, 64>(tw, tx, a, num_sms, stream)
-                         : launch_tile<true, 128>(tw, tx, a, num_sms, stream);
+  if (plan.kind == kLinearToken) {
+    rc = T <= 8 ? launch_token_act<1>(act, x, w, a, stream)
+                : launch_token_act<2>(act, x, w, a, stream);
   } else {
-    rc = plan.bn == 16   ? launch_tile<false, 16>(tw, tx, a, num_sms, stream)
-         : plan.bn == 32 ? launch_tile<false, 32>(tw, tx, a, num_sms, stream)
-         : plan.bn == 64 ? launch_tile<false, 64>(tw, tx, a, num_sms, stream)
-                         : launch_tile<false, 128>(tw, tx, a, num_sms, stream);
+    const bool gated = act == 3, pair = plan.kind == kLinearPair;
+    CUtensorMap tw, tx;
+    if (!make_map_bf16(&tw, w, static_cast<uint64_t>(N) * (gated ? 2 : 1), K,
+                       pair ? plan.bn / 2 : gated ? 64 : 128) ||
+        !make_map_bf16(&tx, x, T, K, pair ? 128 : plan.bn)) {
+      *why = "cuTensorMapEncodeTiled failed for the dense product";
+      return -1;
+    }
+    if (pair) {
+      const bool vec = N % 16 == 0 && reinterpret_cast<uintptr_t>(out) % 32 == 0 &&
+                       reinterpret_cast<uintptr_t>(residual) % 32 == 0;
+      rc = vec ? launch_pair_act<true>(act, tw, tx, a, num_sms, stream)
+               : launch_pair_act<false>(act, tw, tx, a, num_sms, stream);
+    } else {
+      rc = plan.bn == 32   ? launch_row_act<32>(act, tw, tx, a, stream)
+           : plan.bn == 64 ? launch_row_act<64>(act, tw, tx, a, stream)
+                           : launch_row_act<128>(act, tw, tx, a, stream);
+    }
   }
   if (rc != 0) *why = "dense product kernel";
   return rc;

@@ -201,18 +201,19 @@ int launch_add_rms_norm(const void* x, int x_f32, const void* res, int res_f32, 
                         uint8_t* codes, uint8_t* scales, bool vec, cudaStream_t stream);
 
 // ---- dense product (linear.cu) ------------------------------------------------------
+enum LinearKind { kLinearToken, kLinearRow, kLinearPair };
 struct LinearPlan {
-  int bn;         // token columns of a tile
-  int tiles_n;    // weight tiles of 128 output columns
-  int tiles_t;    // token tiles
-  int splits;     // K splits of a tile
-  size_t partial_bytes;
+  LinearKind kind;
+  int bn;         // row tiles: token columns; pair tiles: weight rows of a tile;
+                  // token rows: warps of a CTA
+  int tiles_n, tiles_t;
+  int splits;     // K splits of a tile (CTAs, or pairs, of its cluster)
 };
 LinearPlan plan_linear(int T, int K, int N, bool gated, int num_sms);
 int launch_linear(const void* x, const void* w, const float* bias, int act, const void* residual,
                   int residual_f32, int T, int K, int N, void* out, int out_f32,
-                  const LinearPlan& plan, float* partial, int* tickets, int* err, int num_sms,
-                  cudaStream_t stream, const char** why);
+                  const LinearPlan& plan, int* err, int num_sms, cudaStream_t stream,
+                  const char** why);
 
 // ---- balance loss (balance.cu) --------------------------------------------------------
 // CTAs of the token kernel: eight tokens in flight a CTA, four CTAs an SM.

@@ -64,9 +64,7 @@ def test_linear_refusals(lib):
     assert linear(lib, T=0) == 0
     assert lib.moe_linear_workspace_bytes(4, 60, 32, 0) == 0
     assert lib.moe_linear_workspace_bytes(4, 64, 32, 0) > 0
-    # split partials: a few tokens against many K steps need room for them
-    assert (lib.moe_linear_workspace_bytes(1, 7168, 256, 0)
-            > lib.moe_linear_workspace_bytes(4096, 7168, 8192, 0))
+    assert linear(lib, nbytes=1024) == 1
 
 
 def balance(lib, logits=A, dt=1, ids=A, mask=None, starts=None, B=1, T=4, E=16, k=2, sc=0,
