@@ -379,9 +379,11 @@ int moe_linear(const void* x, const void* w, const float* bias, int act, const v
  *              are not counted; or NULL for the loss and counts alone
  * moe_balance_loss_backward gives dlogits = *dloss * dL/dl from the counts
  * and tokens of a forward call on the same arguments (dloss: fp32 [1], device).
- * Sums of many tokens are in 64 bits and in a fixed order: the same inputs
- * give the same bits.
- * Limits: 1 <= k <= min(E,16), E <= 512, 1 <= B <= 65536, T*k and B*E below 2^31.
+ * Sums over tokens are held as pairs of floats (48 bits) and in a fixed order:
+ * the same inputs give the same bits.
+ * Limits: 1 <= k <= min(E,16), E <= 512, 1 <= B <= 65536, T <= 2^31 - 2^16,
+ * T*k below 2^31.  One launch (cooperative above a few hundred tokens); T = 0
+ * writes zeros.
  * ------------------------------------------------------------------------- */
 size_t moe_balance_loss_workspace_bytes(int T, int E, int B);
 int moe_balance_loss(const void* logits, int logits_dt, const int32_t* topk_ids,

@@ -123,6 +123,7 @@ static const long long* wait_limit_word(void* ws) {
 }
 static_assert(kWsAlignBarrierOffset == MOE_WS_ALIGN_BARRIER_OFFSET, "header layout");
 static_assert(kWsWaitLimitOffset == MOE_WS_WAIT_LIMIT_OFFSET, "header layout");
+static_assert(kWsBalancePartOffset + 8 * kBalanceMaxSms <= kWsRouterTicketOffset, "header layout");
 
 // ---- checks -------------------------------------------------------------------
 // Host-side argument rules of the router (moe_router, moe_router_noalloc and
@@ -606,9 +607,13 @@ int moe_add_rms_norm(const void* x, int x_dt, const void* residual, int residual
   const bool vec = H % 8 == 0 && aligned(x, 16) && aligned(weight, 16) && aligned(residual, 16) &&
                    aligned(residual_out, 16) && aligned(y, 16) && aligned(codes, 16);
   if (codes && !vec) return MOE_ERR_ARG;
+  const bool window = H % 8 != 0 && aligned(x, 16) && aligned(residual, 16) &&
+                      aligned(residual_out, 16) && aligned(y, 16);
+  const int sms = device_num_sms();
+  if (sms <= 0) return cuda_fail("cudaDeviceGetAttribute", cudaGetLastError());
   if (launch_add_rms_norm(x, x_dt == MOE_DT_F32, residual, residual_dt == MOE_DT_F32, weight,
                           weight_dt == MOE_DT_F32, eps, T, H, residual_out, y, codes, scales, vec,
-                          static_cast<cudaStream_t>(stream)) != 0)
+                          window, sms, static_cast<cudaStream_t>(stream)) != 0)
     return launch_fail("norm kernel");
   return MOE_OK;
 }
@@ -651,7 +656,8 @@ int moe_linear(const void* x, const void* w, const float* bias, int act, const v
 static int check_balance(const void* logits, int logits_dt, const int32_t* seq_starts, int B,
                          int T, int E, int scoring, float coef) {
   if (logits_dt != MOE_DT_F32 && logits_dt != MOE_DT_BF16) return MOE_ERR_UNSUPPORTED;
-  if (T < 0 || E <= 0 || E > 512 || B < 1 || B > 65536 || coef != coef) return MOE_ERR_ARG;
+  if (T < 0 || T > 0x7fff0000 || E <= 0 || E > 512 || B < 1 || B > 65536 || coef != coef)
+    return MOE_ERR_ARG;
   if (!seq_starts && B != 1) return MOE_ERR_ARG;
   if (scoring != MOE_SCORING_SOFTMAX && scoring != MOE_SCORING_SIGMOID &&
       scoring != MOE_SCORING_SQRT_SOFTPLUS)
@@ -668,7 +674,7 @@ static bool balance_vec(const void* logits, const void* dlogits, int logits_dt, 
 
 size_t moe_balance_loss_workspace_bytes(int T, int E, int B) {
   if (T < 0 || E <= 0 || E > 512 || B < 1 || B > 65536) return 0;
-  return kWsHeaderBytes + align_up(static_cast<size_t>(balance_grid(T)) * 8, 256);
+  return kWsHeaderBytes;
 }
 
 int moe_balance_loss(const void* logits, int logits_dt, const int32_t* topk_ids,
@@ -683,13 +689,21 @@ int moe_balance_loss(const void* logits, int logits_dt, const int32_t* topk_ids,
   if (!aligned(loss, 4) || !aligned(counts, 4) || !aligned(tokens, 4) || !aligned(topk_ids, 4) ||
       !aligned(dlogits, dt_size(logits_dt)) || !aligned(ws, 256))
     return MOE_ERR_ARG;
-  if (ws_bytes < moe_balance_loss_workspace_bytes(T, E, B)) return MOE_ERR_ARG;
+  if (ws_bytes < kWsHeaderBytes) return MOE_ERR_ARG;
+  const int sms = device_num_sms();
+  if (sms <= 0) return cuda_fail("cudaDeviceGetAttribute", cudaGetLastError());
   char* base = static_cast<char*>(ws);
   if (launch_balance_loss(logits, logits_dt == MOE_DT_BF16, topk_ids, token_mask, seq_starts, B, T,
                           E, k, scoring, coef, loss, counts, tokens, dlogits,
                           balance_vec(logits, dlogits, logits_dt, E),
-                          reinterpret_cast<double*>(base + kWsHeaderBytes),
-                          reinterpret_cast<int*>(base + kWsBalanceTicketOffset), err_word(ws),
+                          reinterpret_cast<float2*>(base + kWsBalancePartOffset),
+                          reinterpret_cast<int*>(base + kWsBalanceOffset),
+                          // align's table of counts: all zeros between calls, too
+                          static_cast<long long>(B) * (E + 1) <= kAlignMaxCtas * kAlignMaxE
+                              ? align_hist(ws)
+                              : nullptr,
+                          err_word(ws),
+                          sms < kBalanceMaxSms ? sms : kBalanceMaxSms,
                           static_cast<cudaStream_t>(stream)) != 0)
     return launch_fail("balance loss kernel");
   return MOE_OK;
@@ -706,9 +720,11 @@ int moe_balance_loss_backward(const float* dloss, const void* logits, int logits
   if (!aligned(dloss, 4) || !aligned(counts, 4) || !aligned(tokens, 4) ||
       !aligned(dlogits, dt_size(logits_dt)))
     return MOE_ERR_ARG;
+  const int sms = device_num_sms();
+  if (sms <= 0) return cuda_fail("cudaDeviceGetAttribute", cudaGetLastError());
   if (launch_balance_loss_backward(dloss, logits, logits_dt == MOE_DT_BF16, counts, tokens,
                                    token_mask, seq_starts, B, T, E, scoring, coef, dlogits,
-                                   balance_vec(logits, dlogits, logits_dt, E),
+                                   balance_vec(logits, dlogits, logits_dt, E), sms,
                                    static_cast<cudaStream_t>(stream)) != 0)
     return launch_fail("balance loss gradient kernel");
   return MOE_OK;

@@ -11,9 +11,17 @@
 //   f_e - sum_j f_j p_j = g_e - sum_j g_j p_j + r
 // keeps the bracket's relative precision, and sum f p = sum g p + 1 - r.
 //
-// Two launches: the counts (integer atomics: any order gives the same sums),
-// then one warp per token that reads the row once.  Each lane owns the same
-// experts for every token, so it keeps their g in registers.
+// One launch: counts, then the tokens, with a barrier over the grid between (a
+// cooperative launch; up to 8 CTAs are one cluster and use its barrier; one
+// CTA needs none).  A CTA owns a run of consecutive tokens.  It counts its
+// assignments in shared memory and adds them to counters in the workspace,
+// which are zero between calls (whole numbers: any order gives the same sums;
+// the last CTA to finish clears them), and loads its first rows while it waits
+// for the others.  Then a group of 16 lanes (32 above 256 experts) takes a
+// token and reads its row once; each lane owns the same experts for every
+// token, so it keeps their g in registers.  Rows come through a ring in shared
+// memory, three ahead of the one computed; two tokens a warp share what is not
+// per expert, and the arithmetic goes in pairs (f32x2).
 #include "moe_common.cuh"
 #include "moe_internal.h"
 
@@ -21,12 +29,9 @@ namespace moe {
 
 namespace {
 
-constexpr int kBalThreads = 256;
-constexpr int kBalWarps = kBalThreads / 32;
-
 struct BalanceArgs {
   const void* logits;
-  const int32_t* ids;
+  const int32_t* ids;  // nullptr: no counting, no loss (the backward call)
   const uint8_t* mask;
   const int32_t* starts;
   int32_t* counts;
@@ -34,320 +39,784 @@ struct BalanceArgs {
   const float* dloss;
   float* loss;
   void* dlogits;
-  double* part;  // [grid] sums of the CTAs
-  int* ticket;
+  float2* part;  // [grid] sums of the CTAs (pairs)
+  int* bars;     // two grid barriers {arrivals, generation}, then the ticket
+  int* acc;      // [B][E + 1] counters, zero between calls: counts, then tokens;
+                 // nullptr (too many): counts and tokens themselves, cleared first
   int* err;
   float coef;
-  int B, T, E, k, scoring;
+  int B, T, E, k;
   int chunk;     // tokens of a CTA
+  int cluster;   // the grid is one cluster
 };
+
+// Starts of the sequences kept in shared memory (more are read from global).
+constexpr int kBalStarts = 1025;
+
+// A barrier over the grid in two halves: all threads of the CTA; what they
+// wrote before arrive is visible to whoever passes wait.  A grid of one
+// cluster uses the hardware's; a larger one (a cooperative launch) counts in
+// the workspace, its wait bounded as every wait.  gen (thread 0) is the
+// barrier's generation, read any time before arrive.
+MOE_DEV int bar_generation(bool cluster, const int* bar) {
+  return !cluster && threadIdx.x == 0 ? load_acquire_gpu(bar + 1) : 0;
+}
+MOE_DEV void bar_arrive(bool cluster, int* bar, int gen) {
+  if (cluster) {
+    cluster_arrive();
+    return;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0 && ticket_add_acq_rel(bar, 1) == static_cast<int>(gridDim.x) - 1) {
+    store_relaxed_gpu(bar, 0);
+    store_release_gpu(bar + 1, gen + 1);
+  }
+}
+MOE_DEV bool bar_wait(bool cluster, int* bar, int gen, int* err) {
+  if (cluster) {
+    cluster_wait();
+    return true;
+  }
+  __shared__ int ok;
+  if (threadIdx.x == 0) {
+    int good = 1;
+    const long long t0 = clock64();
+    while (load_acquire_gpu(bar + 1) == gen) {
+      if (clock64() - t0 > kWaitLimitCycles) {
+        raise_error(err, kErrTimeout);
+        good = 0;
+        break;
+      }
+    }
+    ok = good;
+  }
+  __syncthreads();
+  return ok != 0;
+}
 
 // Sequence of token t: the last one that starts at or before it; -1 when t is
 // before the first start or past the last end.
 MOE_DEV int sequence_of(const int32_t* starts, int B, int t) {
   if (!starts) return 0;
-  if (t < __ldg(starts)) return -1;
+  if (t < starts[0]) return -1;
   int lo = 0, hi = B;  // starts[lo] <= t
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (__ldg(starts + mid) <= t) lo = mid;
+    if (starts[mid] <= t) lo = mid;
     else hi = mid;
   }
-  return t < __ldg(starts + lo + 1) ? lo : -1;
+  return t < starts[lo + 1] ? lo : -1;
 }
 
-__global__ void __launch_bounds__(kBalThreads) balance_count_kernel(const BalanceArgs a) {
-  __shared__ int hist[512];
-  __shared__ int seen;
-  const int t0 = blockIdx.x * a.chunk;
-  const int t1 = static_cast<int>(min(static_cast<long long>(a.T),
-                                      static_cast<long long>(t0) + a.chunk));
-  bool bad = false;
-  for (int t = t0; t < t1;) {
-    // the piece of this CTA's tokens that lies in one sequence
-    const int b = sequence_of(a.starts, a.B, t);
-    int end = t1;
-    if (a.starts) {
-      const int nxt = b >= 0 ? __ldg(a.starts + b + 1) : __ldg(a.starts);
-      if (nxt > t) end = min(end, nxt);
-    }
-    if (b >= 0) {
-      for (int e = threadIdx.x; e < a.E; e += kBalThreads) hist[e] = 0;
-      if (threadIdx.x == 0) seen = 0;
-      __syncthreads();
-      for (long long i = static_cast<long long>(t) * a.k + threadIdx.x;
-           i < static_cast<long long>(end) * a.k; i += kBalThreads) {
-        const int tok = static_cast<int>(i / a.k);
-        if (a.mask && !a.mask[tok]) continue;
-        const int e = __ldg(a.ids + i);
-        if (e >= 0 && e < a.E) atomicAdd(&hist[e], 1);
-        else bad = true;
-        if (i % a.k == 0) atomicAdd(&seen, 1);
-      }
-      __syncthreads();
-      for (int e = threadIdx.x; e < a.E; e += kBalThreads)
-        if (hist[e]) atomicAdd(a.counts + static_cast<size_t>(b) * a.E + e, hist[e]);
-      if (threadIdx.x == 0 && seen) atomicAdd(a.tokens + b, seen);
-      __syncthreads();
-    }
-    t = end;
-  }
-  if (bad) raise_error(a.err, kErrBadExpert);
+// An unevaluated sum of two floats (about 48 bits).  Long sums are held like
+// this and not in fp64, whose rate on this GPU is a small fraction: one 64-bit
+// division and a few additions per warp took as long as the whole kernel does.
+struct Pair {
+  float hi, lo;
+};
+MOE_DEV Pair pair_add(Pair a, Pair b) {
+  const float s = a.hi + b.hi, t = s - a.hi;
+  const float e = (a.hi - (s - t)) + (b.hi - t) + (a.lo + b.lo);
+  const float r = s + e;
+  return {r, e - (r - s)};
 }
-
-MOE_DEV float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+MOE_DEV Pair pair_scale(float c, Pair a) {
+  const float p = c * a.hi;
+  return {p, fmaf(c, a.hi, -p) + c * a.lo};
 }
-MOE_DEV float warp_max(float v) {
+MOE_DEV Pair warp_pair_sum(Pair v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  for (int o = 16; o > 0; o >>= 1)
+    v = pair_add(v, {__shfl_down_sync(0xffffffffu, v.hi, o), __shfl_down_sync(0xffffffffu, v.lo, o)});
   return v;
 }
 
-// Score s(l) and its derivative.
+MOE_DEV float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// Two values at a time: an instruction of the f32x2 kind does both (the token
+// loop is bound by its instructions, not by memory, without them).
+struct Two {
+  unsigned long long v;
+};
+MOE_DEV Two two(float a, float b) {
+  Two r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+MOE_DEV Two two(float a) { return two(a, a); }
+MOE_DEV void split(Two x, float* a, float* b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(*a), "=f"(*b) : "l"(x.v));
+}
+MOE_DEV Two mul2(Two a, Two b) {
+  Two r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+MOE_DEV Two add2(Two a, Two b) {
+  Two r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+MOE_DEV Two fma2(Two a, Two b, Two c) {
+  Two r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
+// e^x for x <= 0 as 2^y: y = x log2(e) in two parts, the hardware's power of
+// two for the first and 1 + z ln 2 for the second (|z| < 2^-16), so that the
+// relative error stays near 2^-22 however small the result is.  Below -120 it
+// is zero; NaN stays NaN.
+MOE_DEV Two exp_neg2(Two v) {
+  constexpr float kLog2e = 1.44269502f;         // log2(e) rounded to a float
+  constexpr float kLog2eRest = 1.92596299e-8f;  // what the rounding left
+  float a, b;
+  split(v, &a, &b);
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(a) : "f"(a), "f"(-120.f));
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(b) : "f"(b), "f"(-120.f));
+  const Two x = two(a, b);
+  const Two y = mul2(x, two(kLog2e));
+  const Two z = fma2(x, two(kLog2eRest), fma2(x, two(kLog2e), mul2(y, two(-1.f))));
+  split(y, &a, &b);
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(a));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(b) : "f"(b));
+  const Two e = two(a, b);
+  return fma2(e, mul2(z, two(0.693147181f)), e);
+}
+
+// Scores s(l) of two logits and their derivatives d, from e = exp(-|l|) <= 1:
+// sigmoid is 1 / (1 + e) or e / (1 + e), and 1 - sigmoid the other one, so
+// neither tail cancels.  l = -inf gives zeros.
 template <int SCORING>
-MOE_DEV void score_of(float l, float* s, float* d) {
+MOE_DEV void score_of(Two l, Two* s, Two* d) {
+  float la, lb;
+  split(l, &la, &lb);
+  const Two e = exp_neg2(two(-fabsf(la), -fabsf(lb)));
+  float a, b, qa, qb;
+  split(add2(e, two(1.f)), &a, &b);
+  a = rcp_approx(a);
+  b = rcp_approx(b);
+  const Two r = two(a, b);
+  const Two q = mul2(e, r);
+  split(q, &qa, &qb);
+  const float sa = la < 0.f ? qa : a, sb = lb < 0.f ? qb : b;
   if constexpr (SCORING == 1) {
-    const float q = 1.f / (1.f + expf(-l));
-    *s = q;
-    *d = q * (1.f / (1.f + expf(l)));  // 1 - q without its cancellation at large l
+    *s = two(sa, sb);
+    *d = mul2(q, r);
   } else {
-    // sqrt(softplus): softplus = max(l, 0) + log1p(e^-|l|); d = sigmoid / (2 s)
-    const float sp = fmaxf(l, 0.f) + log1pf(expf(-fabsf(l)));
-    const float r = sqrtf(sp);
-    *s = r;
-    // below -15, sigmoid = softplus to 32 bits: d = s / 2 (no 0 / 0 at -inf)
-    *d = l < -15.f ? 0.5f * r : 0.5f / (r * (1.f + expf(-l)));
+    // sqrt(softplus), softplus = max(l, 0) + log(1 + e), and log(1 + e) =
+    // 2 atanh(z) with z = e / (2 + e) <= 1/3 by its series (the next term is
+    // below 2^-25 of the sum); d = sigmoid / (2 s)
+    float za, zb;
+    split(add2(e, two(2.f)), &za, &zb);
+    const Two z = mul2(e, two(rcp_approx(za), rcp_approx(zb)));
+    const Two z2 = mul2(z, z);
+    Two p = two(1.f / 15.f);
+    p = fma2(p, z2, two(1.f / 13.f));
+    p = fma2(p, z2, two(1.f / 11.f));
+    p = fma2(p, z2, two(1.f / 9.f));
+    p = fma2(p, z2, two(1.f / 7.f));
+    p = fma2(p, z2, two(1.f / 5.f));
+    p = fma2(p, z2, two(1.f / 3.f));
+    p = fma2(p, z2, two(1.f));
+    float xa, xb, ra, rb;
+    split(fma2(add2(z, z), p, two(la < 0.f ? 0.f : la, lb < 0.f ? 0.f : lb)), &xa, &xb);
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(ra) : "f"(xa));
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(rb) : "f"(xb));
+    *s = two(ra, rb);
+    *d = mul2(mul2(two(0.5f), two(sa, sb)),
+              two(xa == 0.f ? 0.f : rcp_approx(ra), xb == 0.f ? 0.f : rcp_approx(rb)));
   }
 }
 
-// Expert of slot i of a lane: vector loads of four experts (VEC) or one.
-template <bool VEC>
-MOE_DEV int expert_of(int lane, int i) {
-  return VEC ? (i >> 2) * 128 + lane * 4 + (i & 3) : i * 32 + lane;
+// Expert of slot i of lane r of a token's LPT lanes: vector loads of four
+// experts (VEC) or one.
+template <bool VEC, int LPT>
+MOE_DEV int expert_of(int r, int i) {
+  return VEC ? (i >> 2) * (4 * LPT) + r * 4 + (i & 3) : i * LPT + r;
 }
 
-template <bool VEC, int SLOTS, bool BF16>
+// One row, one expert a load; the slots past E are -inf, which scores and
+// weighs nothing.
+template <int SLOTS, bool BF16>
 MOE_DEV void load_row(const void* logits, size_t row, int lane, int E, float (&l)[SLOTS]) {
+#pragma unroll
+  for (int i = 0; i < SLOTS; ++i) {
+    const int e = i * 32 + lane;
+    l[i] = -INFINITY;
+    if (e < E)
+      l[i] = BF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(logits)[row + e])
+                  : static_cast<const float*>(logits)[row + e];
+  }
+}
+
+template <bool VEC, int LPT, int SLOTS, bool BF16>
+MOE_DEV void store_row(void* out, size_t row, int r, int E, const Two (&d)[SLOTS / 2]) {
   if constexpr (VEC) {
 #pragma unroll
     for (int i = 0; i < SLOTS; i += 4) {
-      const int e = expert_of<VEC>(lane, i);
+      const int e = expert_of<VEC, LPT>(r, i);
       if (e < E) {
         if constexpr (BF16) {
-          const uint2 v = __ldg(reinterpret_cast<const uint2*>(
-              static_cast<const __nv_bfloat16*>(logits) + row + e));
-          l[i] = __uint_as_float(v.x << 16);
-          l[i + 1] = __uint_as_float(v.x & 0xFFFF0000u);
-          l[i + 2] = __uint_as_float(v.y << 16);
-          l[i + 3] = __uint_as_float(v.y & 0xFFFF0000u);
+          float a, b, c, f;
+          split(d[i / 2], &a, &b);
+          split(d[i / 2 + 1], &c, &f);
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + row + e) =
+              make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, f));
         } else {
-          const float4 v =
-              __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(logits) + row + e));
-          l[i] = v.x, l[i + 1] = v.y, l[i + 2] = v.z, l[i + 3] = v.w;
+          *reinterpret_cast<ulonglong2*>(static_cast<float*>(out) + row + e) =
+              make_ulonglong2(d[i / 2].v, d[i / 2 + 1].v);
         }
       }
     }
   } else {
 #pragma unroll
     for (int i = 0; i < SLOTS; ++i) {
-      const int e = expert_of<VEC>(lane, i);
-      if (e < E)
-        l[i] = BF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(logits)[row + e])
-                    : static_cast<const float*>(logits)[row + e];
-    }
-  }
-}
-
-template <bool VEC, int SLOTS, bool BF16>
-MOE_DEV void store_row(void* out, size_t row, int lane, int E, const float (&d)[SLOTS]) {
-  if constexpr (VEC) {
-#pragma unroll
-    for (int i = 0; i < SLOTS; i += 4) {
-      const int e = expert_of<VEC>(lane, i);
+      const int e = expert_of<VEC, LPT>(r, i);
+      float a, b;
+      split(d[i / 2], &a, &b);
       if (e < E) {
         if constexpr (BF16)
-          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(out) + row + e) =
-              make_uint2(pack_bf16x2(d[i], d[i + 1]), pack_bf16x2(d[i + 2], d[i + 3]));
+          static_cast<__nv_bfloat16*>(out)[row + e] = __float2bfloat16_rn(i & 1 ? b : a);
         else
-          *reinterpret_cast<float4*>(static_cast<float*>(out) + row + e) =
-              make_float4(d[i], d[i + 1], d[i + 2], d[i + 3]);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < SLOTS; ++i) {
-      const int e = expert_of<VEC>(lane, i);
-      if (e < E) {
-        if constexpr (BF16) static_cast<__nv_bfloat16*>(out)[row + e] = __float2bfloat16_rn(d[i]);
-        else static_cast<float*>(out)[row + e] = d[i];
+          static_cast<float*>(out)[row + e] = i & 1 ? b : a;
       }
     }
   }
 }
 
-// One warp per token; a CTA's warps walk its chunk of consecutive tokens.
-template <int SCORING, bool VEC, int SLOTS, bool BF16>
-__global__ void __launch_bounds__(kBalThreads) balance_token_kernel(const BalanceArgs a) {
-  __shared__ double sums[kBalWarps];
-  __shared__ int nseq, last;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // B': sequences that hold a counted token
-  if (threadIdx.x == 0) nseq = 0;
-  __syncthreads();
-  int mine = 0;
-  for (int b = threadIdx.x; b < a.B; b += kBalThreads) mine += __ldcg(a.tokens + b) > 0;
-  mine = __reduce_add_sync(0xffffffffu, mine);
-  if (lane == 0 && mine) atomicAdd(&nseq, mine);
-  __syncthreads();
-  const int Bp = nseq;
-  const float scale = a.dloss ? a.coef * __ldg(a.dloss) : a.coef;
+constexpr int kBalThreads = 512;  // one CTA an SM, 128 registers a thread (24 warps: slower)
+constexpr int kBalWarps = kBalThreads / 32;
+constexpr int kBalDepth = 4;      // rows of a group's ring
+constexpr int kBalPieces = 4;
 
-  const int t0 = blockIdx.x * a.chunk;
+template <int SCORING, bool VEC, int LPT, int SLOTS, bool BF16>
+__global__ void __launch_bounds__(kBalThreads, 1) balance_kernel(const BalanceArgs a) {
+  constexpr int THREADS = kBalThreads, WARPS = kBalWarps;
+  constexpr int GROUPS = THREADS / LPT;  // tokens that the CTA works on at a time
+  __shared__ int hist[kBalPieces * 512];
+  __shared__ int starts_sm[kBalStarts];
+  __shared__ Pair sums[WARPS];
+  __shared__ int seen[kBalPieces], nseq, last;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int group = threadIdx.x / LPT, r = threadIdx.x % LPT;
+  const int G = gridDim.x;
+  const int t0 = static_cast<int>(min(static_cast<long long>(a.T),
+                                      static_cast<long long>(blockIdx.x) * a.chunk));
   const int t1 = static_cast<int>(min(static_cast<long long>(a.T),
                                       static_cast<long long>(t0) + a.chunk));
-  double acc = 0.0;
-  int cur = -2, until = 0;  // sequence in the registers below, and where it ends
-  float g[SLOTS], share = 0.f;
+  const bool cl = a.cluster != 0;
+  const int gen = a.ids && G > 1 ? bar_generation(cl, a.bars) : 0;
+  if (a.ids) {  // this CTA's ids on their way while the starts are read
+    const char* p = reinterpret_cast<const char*>(a.ids + static_cast<size_t>(t0) * a.k);
+    const size_t bytes = static_cast<size_t>(t1 - t0) * a.k * 4;
+    for (size_t i = threadIdx.x * size_t{128}; i < bytes; i += THREADS * size_t{128})
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(p + i));
+  }
+  const int32_t* starts = a.starts;
+  if (a.starts && a.B < kBalStarts) {
+    for (int i = threadIdx.x; i <= a.B; i += THREADS) starts_sm[i] = __ldg(a.starts + i);
+    starts = starts_sm;
+  }
+  if (threadIdx.x == 0) nseq = 0;
+
+  // This group's rows t0 + group + i GROUPS.  VEC: row i through slot i %
+  // kBalDepth of the group's ring, each lane copying what it reads itself (what
+  // lies past E holds -inf from the start); otherwise one row ahead in
+  // registers.  The first ones are in flight during the counts.
+  extern __shared__ __align__(16) uint8_t ring_raw[];
+  constexpr int LANE_BYTES = BF16 ? 8 : 16;  // four experts
+  constexpr int ROW_BYTES = SLOTS / 4 * LPT * LANE_BYTES;
+  uint8_t* ring = ring_raw + group * kBalDepth * ROW_BYTES + r * LANE_BYTES;
+  const int rows = t0 + group < t1 ? (t1 - t0 - group + GROUPS - 1) / GROUPS : 0;
+  float ahead[VEC ? 1 : SLOTS];
+  auto fetch = [&](int i) {
+    const size_t row = static_cast<size_t>(t0 + group + static_cast<size_t>(i) * GROUPS) * a.E;
+    if constexpr (VEC) {
+      if (i < rows) {
+        const uint32_t dst = smem_u32(ring) + (i % kBalDepth) * ROW_BYTES;
+        const char* src = static_cast<const char*>(a.logits) + (row + r * 4) * (BF16 ? 2 : 4);
 #pragma unroll
-  for (int i = 0; i < SLOTS; ++i) g[i] = 0.f;
-  for (int t = t0 + warp; t < t1; t += kBalWarps) {
-    if (cur == -2 || t >= until) {
-      const int b = sequence_of(a.starts, a.B, t);
-      until = a.starts ? (b >= 0 ? __ldg(a.starts + b + 1) : t + 1) : a.T;
-      if (b != cur) {
-        cur = b;
-        share = 0.f;
-        if (b >= 0) {
-          const int n = __ldcg(a.tokens + b);
-          share = n > 0 ? static_cast<float>(1.0 / (static_cast<double>(Bp) * n)) : 0.f;
-          int c[SLOTS];
-          int placed = 0;
-#pragma unroll
-          for (int i = 0; i < SLOTS; ++i) {
-            const int e = expert_of<VEC>(lane, i);
-            c[i] = e < a.E ? __ldcg(a.counts + static_cast<size_t>(b) * a.E + e) : 0;
-            placed += c[i];
+        for (int j = 0; j < SLOTS / 4; ++j) {
+          if (j * 4 * LPT + r * 4 < a.E) {
+            if constexpr (BF16) cp_async_8(dst + j * LPT * 8, src + j * LPT * 8);
+            else cp_async_16(dst + j * LPT * 16, src + j * LPT * 16, 16);
           }
-          placed = __reduce_add_sync(0xffffffffu, placed);
-          // no assignment placed (all ids bad): f = 0
-          const float inv = placed > 0 ? 1.f / static_cast<float>(placed) : 0.f;
-#pragma unroll
-          for (int i = 0; i < SLOTS; ++i)
-            g[i] = placed > 0 ? static_cast<float>(static_cast<long long>(a.E) * c[i] - placed) * inv
-                              : -1.f;
         }
+      }
+      cp_async_commit();
+    } else {
+      if (i < rows) load_row<SLOTS, BF16>(a.logits, row, r, a.E, ahead);
+    }
+  };
+  auto first_rows = [&]() {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int j = 0; j < SLOTS / 4; ++j)
+        if (j * 4 * LPT + r * 4 >= a.E)
+          for (int i = 0; i < kBalDepth; ++i) {
+            uint32_t* p = reinterpret_cast<uint32_t*>(ring + i * ROW_BYTES + j * LPT * LANE_BYTES);
+            for (int w = 0; w < LANE_BYTES / 4; ++w) p[w] = BF16 ? 0xFF80FF80u : 0xFF800000u;
+          }
+    }
+    fetch(0);
+  };
+  auto more_rows = [&]() {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int i = 1; i < kBalDepth - 1; ++i) fetch(i);
+    }
+  };
+
+  // where the counts are read: one sequence and one CTA, from shared memory;
+  // otherwise cnt[b * pitch + e] and tok[b * tpitch]
+  const bool local = a.ids && G == 1 && !a.starts;
+  int32_t* cnt = a.acc ? a.acc : a.counts;
+  int32_t* tok = a.acc ? a.acc + a.E : a.tokens;
+  const int pitch = a.acc ? a.E + 1 : a.E, tpitch = a.acc ? a.E + 1 : 1;
+  const int cells = a.B * a.E;
+  const int share_of = (cells + G - 1) / G, first = blockIdx.x * share_of;
+  if (a.ids) {
+    bool bad = false, ok = true;
+    if (!a.acc && !local) {
+      for (int i = first + threadIdx.x; i < min(cells, first + share_of); i += THREADS) cnt[i] = 0;
+      for (int i = blockIdx.x * THREADS + threadIdx.x; i < a.B; i += G * THREADS) tok[i] = 0;
+      if (G > 1) {
+        const int gen2 = bar_generation(cl, a.bars + 2);
+        bar_arrive(cl, a.bars + 2, gen2);
+        ok = bar_wait(cl, a.bars + 2, gen2, a.err);
       }
     }
-    const size_t row = static_cast<size_t>(t) * a.E;
-    const bool counted = cur >= 0 && (!a.mask || a.mask[t]);
-    float d[SLOTS];
+    if (starts == starts_sm) __syncthreads();
+    // The CTA's tokens, up to kBalPieces sequences a pass (a CTA that took a
+    // pass for each held up the barrier by 2 us when most have one)
+    for (int t = t0; t < t1;) {
+      int pb[kBalPieces], pe[kBalPieces];  // a piece's sequence and end
+      int end = t, np = 0;
 #pragma unroll
-    for (int i = 0; i < SLOTS; ++i) d[i] = 0.f;
-    if (counted) {
-      float l[SLOTS];
-      load_row<VEC, SLOTS, BF16>(a.logits, row, lane, a.E, l);
-      float sum = 0.f, gs = 0.f;
-      if constexpr (SCORING == 0) {
-        float m = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < SLOTS; ++i)
-          if (expert_of<VEC>(lane, i) < a.E) m = l[i] > m || l[i] != l[i] ? l[i] : m;
-        m = warp_max(m);
-        const float m0 = m == -INFINITY ? 0.f : m;  // all -inf: every term stays zero
-#pragma unroll
-        for (int i = 0; i < SLOTS; ++i) {
-          if (expert_of<VEC>(lane, i) < a.E) d[i] = expf(l[i] - m0);
-          sum += d[i];
-          gs = fmaf(g[i], d[i], gs);
+      for (int j = 0; j < kBalPieces; ++j) {
+        pb[j] = -1;
+        if (end < t1) {
+          const int b = sequence_of(starts, a.B, end);
+          int stop = t1;
+          if (starts) {
+            const int nxt = b >= 0 ? starts[b + 1] : starts[0];
+            if (nxt > end) stop = min(stop, nxt);
+          }
+          pb[j] = b;
+          end = stop;
+          np = j + 1;
         }
-      } else {
+        pe[j] = end;
+      }
+      auto piece_of = [&](int token) {
+        int j = 0;
 #pragma unroll
-        for (int i = 0; i < SLOTS; ++i) {
-          float s = 0.f;
-          if (expert_of<VEC>(lane, i) < a.E) score_of<SCORING>(l[i], &s, &d[i]);
-          sum += s;
-          gs = fmaf(g[i], s, gs);
+        for (int i = 0; i + 1 < kBalPieces; ++i) j += token >= pe[i];
+        return j;
+      };
+      auto sequence_at = [&](int j) {
+        int b = pb[0];
+#pragma unroll
+        for (int i = 1; i < kBalPieces; ++i) b = j == i ? pb[i] : b;
+        return b;
+      };
+      const unsigned n = static_cast<unsigned>(end - t) * a.k;
+      const int32_t* ids = a.ids + static_cast<size_t>(t) * a.k;
+      constexpr int U = 8;  // ids of a thread in flight
+      int e[U], into[U];    // expert, and piece (-1: not counted)
+      auto load_ids = [&](unsigned i0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const unsigned i = i0 + u * THREADS;
+          e[u] = i < n ? __ldg(ids + i) : -1;
+          into[u] = i < n ? 0 : -1;
+          if (i < n && (a.mask || np > 1 || pb[0] < 0)) {
+            const int token = t + static_cast<int>(i / a.k);
+            const int j = piece_of(token);
+            into[u] = sequence_at(j) >= 0 && (!a.mask || a.mask[token] != 0) ? j : -1;
+          }
+        }
+      };
+      load_ids(threadIdx.x);
+      int marked[kBalPieces];
+#pragma unroll
+      for (int j = 0; j < kBalPieces; ++j) marked[j] = 0;
+      if (a.mask) {
+        for (int i = t + threadIdx.x; i < end; i += THREADS) {
+          const int m = a.mask[i] != 0, at = piece_of(i);
+#pragma unroll
+          for (int j = 0; j < kBalPieces; ++j) marked[j] += j == at ? m : 0;
         }
       }
-      sum = warp_sum(sum);
-      gs = warp_sum(gs);
-      float inv, rest;  // 1 / normaliser, 1 - sum p
-      if constexpr (SCORING == 0) {
-        inv = sum == 0.f ? 0.f : 1.f / sum;
-        rest = sum == 0.f ? 1.f : 0.f;
-      } else {
-        inv = 1.f / (sum + 1e-20f);
-        rest = 1e-20f * inv;
+      for (int i = threadIdx.x; i < np * 512; i += THREADS) hist[i] = 0;
+      if (threadIdx.x < kBalPieces) {
+        const int j = threadIdx.x;
+        const int from = j == 0 ? t : j == 1 ? pe[0] : j == 2 ? pe[1] : pe[2];
+        const int to = j == 0 ? pe[0] : j == 1 ? pe[1] : j == 2 ? pe[2] : pe[3];
+        seen[j] = a.mask ? 0 : to - from;
       }
-      const float mean = gs * inv - rest;  // sum f p - 1
-      acc += static_cast<double>(share) * (1.0 + static_cast<double>(mean));
-      const float c = share * scale * inv;
+      __syncthreads();
+      for (unsigned i0 = threadIdx.x; i0 < n;) {
 #pragma unroll
-      for (int i = 0; i < SLOTS; ++i) d[i] = c * d[i] * (g[i] - mean);
+        for (int u = 0; u < U; ++u) {
+          if (into[u] >= 0) {
+            if (e[u] >= 0 && e[u] < a.E) atomicAdd(&hist[into[u] * 512 + e[u]], 1);
+            else bad = true;
+          }
+        }
+        i0 += U * THREADS;
+        if (i0 < n) load_ids(i0);
+      }
+      if (a.mask) {
+#pragma unroll
+        for (int j = 0; j < kBalPieces; ++j) {
+          const int c = __reduce_add_sync(0xffffffffu, marked[j]);
+          if (lane == 0 && c) atomicAdd(&seen[j], c);
+        }
+      }
+      __syncthreads();
+      if (local) {
+        for (int i = threadIdx.x; i < a.E; i += THREADS) a.counts[i] = hist[i];
+        if (threadIdx.x == 0) a.tokens[0] = seen[0];
+      } else {
+#pragma unroll
+        for (int j = 0; j < kBalPieces; ++j) {
+          if (pb[j] >= 0) {
+            for (int i = threadIdx.x; i < a.E; i += THREADS)
+              if (hist[j * 512 + i])
+                atomicAdd(cnt + static_cast<size_t>(pb[j]) * pitch + i, hist[j * 512 + i]);
+            if (threadIdx.x == 0 && seen[j])
+              atomicAdd(tok + static_cast<size_t>(pb[j]) * tpitch, seen[j]);
+          }
+        }
+        if (end < t1) __syncthreads();
+      }
+      t = end;
     }
-    if (a.dlogits) store_row<VEC, SLOTS, BF16>(a.dlogits, row, lane, a.E, d);
+    if (bad) raise_error(a.err, kErrBadExpert);
+    // (only the first rows in front of the barrier: the others' traffic would
+    // hold up its messages)
+    if (G > 1) {
+      bar_arrive(cl, a.bars, gen);
+      first_rows();
+      ok = bar_wait(cl, a.bars, gen, a.err) && ok;
+      if (!ok) return;  // flagged; the outputs are not valid
+    } else {
+      first_rows();
+      __syncthreads();
+    }
+    more_rows();
+  } else {
+    first_rows();
+    more_rows();
+    __syncthreads();
+  }
+  // the counts of the CTA's first sequence to shared memory, once: every group
+  // of every CTA reading them from the same few lines of L2 took 4 us
+  const int bfirst = t0 < t1 ? sequence_of(starts, a.B, t0) : -1;
+  if (!local && bfirst >= 0) {
+    for (int i = threadIdx.x; i < a.E; i += THREADS)
+      hist[i] = __ldcg(cnt + static_cast<size_t>(bfirst) * pitch + i);
+    if (threadIdx.x == 0) seen[0] = __ldcg(tok + static_cast<size_t>(bfirst) * tpitch);
+  }
+
+  // the experts' g of one sequence, and how much of the loss a token of it is
+  Two g[SLOTS / 2];
+  float share = 0.f;
+#pragma unroll
+  for (int i = 0; i < SLOTS / 2; ++i) g[i] = two(0.f);
+  int Bp = 0;
+  int cur = -2, until = t0;  // that sequence, and where it ends
+  auto load_counts = [&](int b, int (&c)[SLOTS]) {
+#pragma unroll
+    for (int i = 0; i < SLOTS; ++i) {
+      const int e = expert_of<VEC, LPT>(r, i);
+      c[i] = 0;
+      if (b >= 0 && e < a.E)
+        c[i] = b == bfirst ? hist[e] : __ldcg(cnt + static_cast<size_t>(b) * pitch + e);
+    }
+  };
+  auto load_tokens = [&](int b) {
+    return b < 0 ? 0 : b == bfirst ? seen[0] : __ldcg(tok + static_cast<size_t>(b) * tpitch);
+  };
+  // (all lanes of the warp)
+  auto enter = [&](int n, const int (&c)[SLOTS]) {
+    share = n > 0 ? 1.f / static_cast<float>(n) / static_cast<float>(Bp) : 0.f;
+    int placed = 0;
+#pragma unroll
+    for (int i = 0; i < SLOTS; ++i) placed += c[i];
+#pragma unroll
+    for (int o = LPT / 2; o > 0; o >>= 1) placed += __shfl_xor_sync(0xffffffffu, placed, o);
+    // no assignment placed (all ids bad): f = 0
+    const float A = static_cast<float>(placed), E = static_cast<float>(a.E);
+    const float inv = placed > 0 ? 1.f / A : 0.f;
+    if (__any_sync(0xffffffffu, placed >= 1 << 24)) {
+      const long long wide = a.E;
+#pragma unroll
+      for (int i = 0; i < SLOTS / 2; ++i)
+        g[i] = two(static_cast<float>(wide * c[2 * i] - placed) * inv,
+                   static_cast<float>(wide * c[2 * i + 1] - placed) * inv);
+    } else {  // counts are exact floats, and the product and difference one fma
+#pragma unroll
+      for (int i = 0; i < SLOTS / 2; ++i)
+        g[i] = two(fmaf(E, static_cast<float>(c[2 * i]), -A) * inv,
+                   fmaf(E, static_cast<float>(c[2 * i + 1]), -A) * inv);
+    }
+    if (placed == 0) {
+#pragma unroll
+      for (int i = 0; i < SLOTS / 2; ++i) g[i] = two(-1.f);
+    }
+  };
+  // B': the sequences that hold a counted token
+  if (a.starts) {
+    int mine = 0;
+    for (int i = threadIdx.x; i < a.B; i += THREADS)
+      mine += __ldcg(tok + static_cast<size_t>(i) * tpitch) > 0;
+    mine = __reduce_add_sync(0xffffffffu, mine);
+    if (lane == 0 && mine) atomicAdd(&nseq, mine);
+  }
+  __syncthreads();
+  Bp = a.starts ? nseq : 1;  // (without a counted token no share is taken)
+  {
+    const int t = t0 + group;
+    if (t < t1) {
+      cur = sequence_of(starts, a.B, t);
+      until = !starts ? a.T : cur >= 0 ? starts[cur + 1] : t + 1;
+    }
+    int c[SLOTS];
+    load_counts(cur, c);
+    enter(load_tokens(cur), c);
+  }
+  if (a.ids && a.acc && !local) {
+    for (int i = first + threadIdx.x; i < min(cells, first + share_of); i += THREADS)
+      a.counts[i] = __ldcg(cnt + i + i / a.E);  // pitch E + 1
+    for (int i = blockIdx.x * THREADS + threadIdx.x; i < a.B; i += G * THREADS)
+      a.tokens[i] = __ldcg(tok + static_cast<size_t>(i) * tpitch);
+  }
+  const float scale = a.dloss ? a.coef * __ldg(a.dloss) : a.coef;
+
+  // sum of share * (1 + mean) over this group's tokens, share being the same
+  // through a sequence
+  Pair acc = {0.f, 0.f}, means = {0.f, 0.f};
+  int held = 0;
+  auto fold = [&](float c) {
+    acc = pair_add(acc, pair_scale(c, pair_add({static_cast<float>(held), 0.f}, means)));
+    means = {0.f, 0.f};
+    held = 0;
+  };
+  const int warp_rows = __shfl_sync(0xffffffffu, rows, 0);  // of the warp's first group: the most
+  unsigned marks = 0;  // bit of lane r: whether row i + r of its group is counted
+#pragma unroll 1
+  for (int i = 0; i < warp_rows; ++i) {
+    const int t = t0 + group + i * GROUPS;
+    const bool live = i < rows;
+    if (i % LPT == 0)
+      marks = __ballot_sync(0xffffffffu,
+                            i + r < rows && (!a.mask || a.mask[t + r * GROUPS] != 0));
+    if (__any_sync(0xffffffffu, live && t >= until)) {
+      const bool move = live && t >= until;
+      int b = cur;
+      if (move) {
+        b = sequence_of(starts, a.B, t);
+        until = !starts ? a.T : b >= 0 ? starts[b + 1] : t + 1;
+      }
+      if (__any_sync(0xffffffffu, b != cur)) {
+        if (held) fold(share);
+        cur = b;
+        int c[SLOTS];
+        load_counts(b, c);
+        enter(load_tokens(b), c);
+      }
+    }
+    const bool on = live && cur >= 0 && ((marks >> ((lane & ~(LPT - 1)) + i % LPT)) & 1u);
+    Two x[SLOTS / 2];
+    if constexpr (VEC) {
+      fetch(i + kBalDepth - 1);
+      cp_async_wait<kBalDepth - 1>();  // row i has landed
+#pragma unroll
+      for (int j = 0; j < SLOTS / 4; ++j) {
+        const uint8_t* src = ring + (i % kBalDepth) * ROW_BYTES + j * LPT * LANE_BYTES;
+        if constexpr (BF16) {
+          const uint2 v = *reinterpret_cast<const uint2*>(src);
+          x[2 * j] = two(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u));
+          x[2 * j + 1] = two(__uint_as_float(v.y << 16), __uint_as_float(v.y & 0xFFFF0000u));
+        } else {
+          const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(src);
+          x[2 * j].v = v.x;
+          x[2 * j + 1].v = v.y;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < SLOTS / 2; ++j) x[j] = two(ahead[2 * j], ahead[2 * j + 1]);
+      fetch(i + 1);
+    }
+    Two s2 = two(0.f), g2 = two(0.f), d[SLOTS / 2];
+    if constexpr (SCORING == 0) {
+      float m = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < SLOTS / 2; ++j) {
+        float p, q;
+        split(x[j], &p, &q);
+        m = fmaxf(m, fmaxf(p, q));  // (a NaN shows in the sums)
+      }
+#pragma unroll
+      for (int o = LPT / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const Two m2 = two(m == -INFINITY ? 0.f : -m);  // all -inf: every term stays zero
+#pragma unroll
+      for (int j = 0; j < SLOTS / 2; ++j) {
+        d[j] = exp_neg2(add2(x[j], m2));
+        s2 = add2(s2, d[j]);
+        g2 = fma2(g[j], d[j], g2);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < SLOTS / 2; ++j) {
+        Two s;
+        score_of<SCORING>(x[j], &s, &d[j]);
+        s2 = add2(s2, s);
+        g2 = fma2(g[j], s, g2);
+      }
+    }
+    float sum, gs, p, q;
+    split(s2, &p, &q);
+    sum = p + q;
+    split(g2, &p, &q);
+    gs = p + q;
+#pragma unroll
+    for (int o = LPT / 2; o > 0; o >>= 1) {
+      sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      gs += __shfl_xor_sync(0xffffffffu, gs, o);
+    }
+    float inv, rest;  // 1 / normaliser, 1 - sum p
+    if constexpr (SCORING == 0) {
+      inv = sum == 0.f ? 0.f : rcp_approx(sum);
+      rest = sum == 0.f ? 1.f : 0.f;
+    } else {
+      inv = rcp_approx(sum + 1e-20f);
+      rest = 1e-20f * inv;
+    }
+    const float mean = gs * inv - rest;  // sum f p - 1
+    if (on) {
+      means = pair_add(means, {mean, 0.f});
+      ++held;
+    }
+    if (a.dlogits && live) {
+      const Two c2 = two(share * scale * inv), m2 = two(-mean);
+#pragma unroll
+      for (int j = 0; j < SLOTS / 2; ++j)
+        d[j] = on ? mul2(mul2(c2, d[j]), add2(g[j], m2)) : two(0.f);
+      store_row<VEC, LPT, SLOTS, BF16>(a.dlogits, static_cast<size_t>(t) * a.E, r, a.E, d);
+    }
   }
   if (!a.loss) return;
-  // the CTAs' sums in a fixed order, by the last CTA to finish
+  if (held) fold(share);
+  // the CTAs' sums in a fixed order, by the last CTA to finish, which also
+  // clears the counters: every other CTA has read them
+  acc = warp_pair_sum(r == 0 ? acc : Pair{0.f, 0.f});
   if (lane == 0) sums[warp] = acc;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    double s = 0.0;
-    for (int w = 0; w < kBalWarps; ++w) s += sums[w];
-    __stcg(a.part + blockIdx.x, s);
-    last = ticket_add_acq_rel(a.ticket, 1) == static_cast<int>(gridDim.x) - 1;
-    if (last) store_relaxed_gpu(a.ticket, 0);
-  }
-  __syncthreads();
-  if (last) {
-    double s = 0.0;
-    for (int i = threadIdx.x; i < static_cast<int>(gridDim.x); i += kBalThreads)
-      s += __ldcg(a.part + i);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) sums[warp] = s;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      s = 0.0;
-      for (int w = 0; w < kBalWarps; ++w) s += sums[w];
-      *a.loss = static_cast<float>(s * a.coef);
+  if (warp == 0) {
+    Pair s = warp_pair_sum(lane < WARPS ? sums[lane] : Pair{0.f, 0.f});
+    if (lane == 0) {
+      if (G == 1) {
+        *a.loss = pair_scale(a.coef, s).hi;
+        last = 1;
+      } else {
+        __stcg(a.part + blockIdx.x, make_float2(s.hi, s.lo));
+        last = ticket_add_acq_rel(a.bars + 4, 1) == G - 1;
+        if (last) store_relaxed_gpu(a.bars + 4, 0);
+      }
+    }
+    __syncwarp();
+    if (last && G > 1) {
+      s = {0.f, 0.f};
+      for (int i = lane; i < G; i += 32) {
+        const float2 f = __ldcg(a.part + i);
+        s = pair_add(s, {f.x, f.y});
+      }
+      s = warp_pair_sum(s);
+      if (lane == 0) *a.loss = pair_scale(a.coef, s).hi;
     }
   }
+  if (local || !a.acc) return;
+  __syncthreads();
+  if (last)
+    for (int i = threadIdx.x; i < a.B * (a.E + 1); i += THREADS) a.acc[i] = 0;
+}
+
+// Tokens a group would get from one CTA up to which one CTA, or one cluster of
+// 8, is launched (measured in a graph, 256 experts, see the figures above).
+constexpr int kBalOneCta = 3;
+constexpr int kBalCluster = 16;
+
+template <int SCORING, bool VEC, int LPT, int SLOTS, bool BF16>
+int launch_one(BalanceArgs a, int num_sms, cudaStream_t st) {
+  constexpr int GROUPS = kBalThreads / LPT;
+  // One CTA, one cluster of up to 8, or every SM: more CTAs share the tokens,
+  // but meet at slower barriers (see kBal*Tokens).
+  int grid = 1, cluster = 1;
+  const int per = (a.T + GROUPS - 1) / GROUPS;  // CTAs at one token a group
+  if (per > kBalOneCta) {
+    if (per <= kBalCluster) {
+      grid = cluster = per < 8 ? per : 8;
+    } else {
+      grid = per < num_sms ? per : num_sms;
+    }
+  }
+  a.chunk = static_cast<int>((static_cast<long long>(a.T) + grid - 1) / grid);
+  a.cluster = cluster > 1;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kBalThreads);
+  cfg.dynamicSmemBytes = VEC ? kBalThreads * kBalDepth * SLOTS * (BF16 ? 2 : 4) : 0;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  static std::atomic<unsigned long long> smem_set{0};
+  const auto kernel = balance_kernel<SCORING, VEC, LPT, SLOTS, BF16>;
+  if (VEC && !ensure_smem_limit(reinterpret_cast<const void*>(kernel),
+                                static_cast<int>(cfg.dynamicSmemBytes), smem_set))
+    return -1;
+  if (cluster > 1) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.numAttrs = 1;
+  } else if (a.ids && grid > 1) {
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+    cfg.numAttrs = 1;
+  }
+  if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) return -1;
+  return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
 
 template <int SCORING, bool BF16>
-void launch_slots(const BalanceArgs& a, bool vec, int grid, cudaStream_t st) {
-  if (vec) {
-    if (a.E <= 128) balance_token_kernel<SCORING, true, 4, BF16><<<grid, kBalThreads, 0, st>>>(a);
-    else if (a.E <= 256) balance_token_kernel<SCORING, true, 8, BF16><<<grid, kBalThreads, 0, st>>>(a);
-    else if (a.E <= 384) balance_token_kernel<SCORING, true, 12, BF16><<<grid, kBalThreads, 0, st>>>(a);
-    else balance_token_kernel<SCORING, true, 16, BF16><<<grid, kBalThreads, 0, st>>>(a);
-  } else {
-    if (a.E <= 32) balance_token_kernel<SCORING, false, 1, BF16><<<grid, kBalThreads, 0, st>>>(a);
-    else if (a.E <= 64) balance_token_kernel<SCORING, false, 2, BF16><<<grid, kBalThreads, 0, st>>>(a);
-    else if (a.E <= 128) balance_token_kernel<SCORING, false, 4, BF16><<<grid, kBalThreads, 0, st>>>(a);
-    else if (a.E <= 256) balance_token_kernel<SCORING, false, 8, BF16><<<grid, kBalThreads, 0, st>>>(a);
-    else balance_token_kernel<SCORING, false, 16, BF16><<<grid, kBalThreads, 0, st>>>(a);
-  }
+int launch_slots(const BalanceArgs& a, bool vec, int sms, cudaStream_t st) {
+  if (vec)
+    return a.E <= 128   ? launch_one<SCORING, true, 16, 8, BF16>(a, sms, st)
+           : a.E <= 256 ? launch_one<SCORING, true, 16, 16, BF16>(a, sms, st)
+           : a.E <= 384 ? launch_one<SCORING, true, 32, 12, BF16>(a, sms, st)
+                        : launch_one<SCORING, true, 32, 16, BF16>(a, sms, st);
+  return a.E <= 64    ? launch_one<SCORING, false, 32, 2, BF16>(a, sms, st)
+         : a.E <= 256 ? launch_one<SCORING, false, 32, 8, BF16>(a, sms, st)
+                      : launch_one<SCORING, false, 32, 16, BF16>(a, sms, st);
 }
 
-int launch_tokens(BalanceArgs a, bool bf16, bool vec, cudaStream_t st) {
-  const int grid = balance_grid(a.T);
-  a.chunk = (a.T + grid - 1) / grid;
-  if (a.scoring == 0) {
-    if (bf16) launch_slots<0, true>(a, vec, grid, st);
-    else launch_slots<0, false>(a, vec, grid, st);
-  } else if (a.scoring == 1) {
-    if (bf16) launch_slots<1, true>(a, vec, grid, st);
-    else launch_slots<1, false>(a, vec, grid, st);
-  } else {
-    if (bf16) launch_slots<2, true>(a, vec, grid, st);
-    else launch_slots<2, false>(a, vec, grid, st);
-  }
-  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+int launch_scoring(const BalanceArgs& a, int scoring, bool bf16, bool vec, int sms,
+                   cudaStream_t st) {
+  if (scoring == 0)
+    return bf16 ? launch_slots<0, true>(a, vec, sms, st) : launch_slots<0, false>(a, vec, sms, st);
+  if (scoring == 1)
+    return bf16 ? launch_slots<1, true>(a, vec, sms, st) : launch_slots<1, false>(a, vec, sms, st);
+  return bf16 ? launch_slots<2, true>(a, vec, sms, st) : launch_slots<2, false>(a, vec, sms, st);
 }
 
 }  // namespace
@@ -355,11 +824,14 @@ int launch_tokens(BalanceArgs a, bool bf16, bool vec, cudaStream_t st) {
 int launch_balance_loss(const void* logits, bool bf16, const int32_t* ids, const uint8_t* mask,
                         const int32_t* starts, int B, int T, int E, int k, int scoring,
                         float coef, float* loss, int32_t* counts, int32_t* tokens, void* dlogits,
-                        bool vec, double* part, int* ticket, int* err, cudaStream_t st) {
-  if (cudaMemsetAsync(counts, 0, static_cast<size_t>(B) * E * 4, st) != cudaSuccess ||
-      cudaMemsetAsync(tokens, 0, static_cast<size_t>(B) * 4, st) != cudaSuccess)
-    return -1;
-  if (T == 0) return cudaMemsetAsync(loss, 0, 4, st) == cudaSuccess ? 0 : -1;
+                        bool vec, float2* part, int* bars, int* acc, int* err, int num_sms,
+                        cudaStream_t st) {
+  if (T == 0) {
+    const bool done = cudaMemsetAsync(counts, 0, static_cast<size_t>(B) * E * 4, st) == cudaSuccess &&
+                      cudaMemsetAsync(tokens, 0, static_cast<size_t>(B) * 4, st) == cudaSuccess &&
+                      cudaMemsetAsync(loss, 0, 4, st) == cudaSuccess;
+    return done ? 0 : -1;
+  }
   BalanceArgs a{};
   a.logits = logits;
   a.ids = ids;
@@ -370,25 +842,21 @@ int launch_balance_loss(const void* logits, bool bf16, const int32_t* ids, const
   a.loss = loss;
   a.dlogits = dlogits;
   a.part = part;
-  a.ticket = ticket;
+  a.bars = bars;
+  a.acc = acc;
   a.err = err;
   a.coef = coef;
   a.B = B;
   a.T = T;
   a.E = E;
   a.k = k;
-  a.scoring = scoring;
-  const int grid = balance_grid(T);
-  a.chunk = (T + grid - 1) / grid;
-  balance_count_kernel<<<grid, kBalThreads, 0, st>>>(a);
-  if (cudaGetLastError() != cudaSuccess) return -1;
-  return launch_tokens(a, bf16, vec, st);
+  return launch_scoring(a, scoring, bf16, vec, num_sms, st);
 }
 
 int launch_balance_loss_backward(const float* dloss, const void* logits, bool bf16,
                                  const int32_t* counts, const int32_t* tokens,
                                  const uint8_t* mask, const int32_t* starts, int B, int T, int E,
-                                 int scoring, float coef, void* dlogits, bool vec,
+                                 int scoring, float coef, void* dlogits, bool vec, int num_sms,
                                  cudaStream_t st) {
   BalanceArgs a{};
   a.logits = logits;
@@ -402,8 +870,7 @@ int launch_balance_loss_backward(const float* dloss, const void* logits, bool bf
   a.B = B;
   a.T = T;
   a.E = E;
-  a.scoring = scoring;
-  return launch_tokens(a, bf16, vec, st);
+  return launch_scoring(a, scoring, bf16, vec, num_sms, st);
 }
 
 }  // namespace moe

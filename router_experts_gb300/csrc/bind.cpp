@@ -1,0 +1,342 @@
+// bind.cpp -- Python binding of the operators around the layer (add_rms_norm,
+// linear, balance_loss, balance_loss_backward): the checks of the tensors and
+// the marshalling into the C ABI of include/moe.h.
+//
+// These operators take a few microseconds on the GPU for one token, less than
+// checking and converting their arguments costs in Python (about 8 us for the
+// norm's seven tensors through ctypes; 0.5 us here), so this part is native.
+// There is no fallback: the functions only check, allocate outputs that the
+// caller did not pass, and call the library on the current stream.
+#include <Python.h>
+
+#include <ATen/core/Tensor.h>
+#include <ATen/ops/empty.h>
+#include <ATen/ops/empty_like.h>
+#include <c10/cuda/CUDAGuard.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <initializer_list>
+#include <stdexcept>
+#include <string>
+
+#include "../../include/moe.h"
+
+namespace {
+
+using at::ScalarType;
+using at::Tensor;
+
+struct ValueError : std::runtime_error {
+  using std::runtime_error::runtime_error;
+};
+
+std::string shape_text(at::IntArrayRef s) {
+  std::string t = "(";
+  for (size_t i = 0; i < s.size(); ++i) t += (i ? ", " : "") + std::to_string(s[i]);
+  return t + ")";
+}
+
+// None -> nullptr.
+const Tensor* tensor(PyObject* o, const char* name) {
+  if (o == Py_None) return nullptr;
+  if (!THPVariable_Check(o)) throw ValueError(std::string(name) + ": expected a tensor");
+  return &THPVariable_Unpack(o);
+}
+const Tensor& required(PyObject* o, const char* name) {
+  const Tensor* t = tensor(o, name);
+  if (!t) throw ValueError(std::string(name) + ": expected a tensor, got None");
+  return *t;
+}
+const Tensor& matrix(PyObject* o, const char* name) {
+  const Tensor& t = required(o, name);
+  if (t.dim() != 2)
+    throw ValueError(std::string(name) + ": expected a matrix, got shape " +
+                     shape_text(t.sizes()));
+  return t;
+}
+
+// Device address of a tensor after the checks that keep the kernels inside it.
+void* address(const Tensor* t, const char* name, c10::Device dev,
+              std::initializer_list<ScalarType> types, std::initializer_list<int64_t> shape) {
+  if (!t) return nullptr;
+  if (!t->is_cuda() || t->device() != dev)
+    throw ValueError(std::string(name) + ": expected a CUDA tensor on " + dev.str() +
+                     ", got one on " + t->device().str());
+  bool known = false;
+  for (ScalarType s : types) known = known || t->scalar_type() == s;
+  if (!known)
+    throw ValueError(std::string(name) + ": unsupported dtype " + c10::toString(t->scalar_type()));
+  if (t->sizes() != at::IntArrayRef(shape))
+    throw ValueError(std::string(name) + ": expected shape " +
+                     shape_text(at::IntArrayRef(shape)) + ", got " + shape_text(t->sizes()));
+  if (!t->is_contiguous())
+    throw ValueError(std::string(name) + ": expected a contiguous tensor, got strides " +
+                     shape_text(t->strides()));
+  return t->data_ptr();
+}
+void* address(const Tensor& t, const char* name, c10::Device dev,
+              std::initializer_list<ScalarType> types, std::initializer_list<int64_t> shape) {
+  return address(&t, name, dev, types, shape);
+}
+
+int as_int(int64_t v, const char* name) {
+  if (v < 0 || v > 0x7fffffff) throw ValueError(std::string(name) + ": size past 32 bits");
+  return static_cast<int>(v);
+}
+int dt_code(const Tensor* t) {
+  return t && t->scalar_type() == at::kFloat ? MOE_DT_F32 : MOE_DT_BF16;
+}
+int64_t long_arg(PyObject* o) {
+  const long long v = PyLong_AsLongLong(o);
+  if (v == -1 && PyErr_Occurred()) throw std::exception();
+  return v;
+}
+float float_arg(PyObject* o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw std::exception();
+  return static_cast<float>(v);
+}
+bool bool_arg(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw std::exception();
+  return v != 0;
+}
+void expect_args(Py_ssize_t n, Py_ssize_t want) {
+  if (n != want) throw ValueError("wrong number of arguments");
+}
+
+// Every launch goes to the tensors' device, on its current stream.
+struct Launch {
+  c10::cuda::OptionalCUDAGuard guard;
+  void* stream = nullptr;
+  explicit Launch(c10::Device dev) {
+    guard.set_device(dev);
+    stream = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
+  }
+};
+
+PyObject* status(int rc) { return PyLong_FromLong(rc); }
+
+// f's result, or the Python exception for what it throws.
+template <class F>
+PyObject* guarded(F&& f) noexcept {
+  try {
+    return f();
+  } catch (const ValueError& e) {
+    PyErr_SetString(PyExc_ValueError, e.what());
+  } catch (const std::exception& e) {
+    if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
+  }
+  return nullptr;
+}
+
+PyObject* wrap(const Tensor& t) {
+  if (!t.defined()) Py_RETURN_NONE;
+  return THPVariable_Wrap(t);
+}
+// (status, out...) as a Python tuple.
+PyObject* result(int rc, std::initializer_list<Tensor> out) {
+  PyObject* r = PyTuple_New(1 + static_cast<Py_ssize_t>(out.size()));
+  if (!r) return nullptr;
+  PyTuple_SET_ITEM(r, 0, status(rc));
+  Py_ssize_t i = 1;
+  for (const Tensor& t : out) {
+    PyObject* o = wrap(t);
+    if (!o) {
+      Py_DECREF(r);
+      return nullptr;
+    }
+    PyTuple_SET_ITEM(r, i++, o);
+  }
+  return r;
+}
+// Item i of `out` (a tuple of n), undefined for None.
+Tensor out_item(PyObject* out, Py_ssize_t n, Py_ssize_t i, const char* name) {
+  if (!PyTuple_Check(out) || PyTuple_GET_SIZE(out) != n)
+    throw ValueError("out: expected a tuple of " + std::to_string(n));
+  const Tensor* t = tensor(PyTuple_GET_ITEM(out, i), name);
+  return t ? *t : Tensor();
+}
+const Tensor* ptr(const Tensor& t) { return t.defined() ? &t : nullptr; }
+
+// (x, weight, residual, eps, y, e4m3, out) -> (status, residual_out, y, codes, scales)
+PyObject* add_rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    expect_args(n, 7);
+    const Tensor& x = matrix(a[0], "x");
+    const Tensor& w = required(a[1], "weight");
+    const Tensor* res = tensor(a[2], "residual");
+    const bool want_y = bool_arg(a[4]), want_q = bool_arg(a[5]);
+    const int64_t T = x.size(0), H = x.size(1);
+    if (!want_y && !want_q) throw ValueError("nothing to write: y and e4m3 are both False");
+    if (want_q && H % 32 != 0)
+      throw ValueError("e4m3 needs whole groups of 32 values, got rows of " + std::to_string(H));
+    const c10::Device dev = x.device();
+    void* xp = address(x, "x", dev, {at::kBFloat16, at::kFloat}, {T, H});
+    void* wp = address(w, "weight", dev, {at::kBFloat16, at::kFloat}, {H});
+    void* rp = address(res, "residual", dev, {at::kBFloat16, at::kFloat}, {T, H});
+    Tensor ro, y, codes, scales;
+    if (a[6] == Py_None) {
+      if (res) ro = at::empty_like(*res);
+      if (want_y) y = at::empty({T, H}, x.options().dtype(at::kBFloat16));
+      if (want_q) {
+        codes = at::empty({T, H}, x.options().dtype(at::kByte));
+        scales = at::empty({T, H / 32}, x.options().dtype(at::kByte));
+      }
+    } else {
+      ro = out_item(a[6], 4, 0, "residual_out");
+      y = out_item(a[6], 4, 1, "y");
+      codes = out_item(a[6], 4, 2, "codes");
+      scales = out_item(a[6], 4, 3, "scales");
+      if (ro.defined() != (res != nullptr) || y.defined() != want_y ||
+          codes.defined() != want_q || scales.defined() != want_q)
+        throw ValueError("out does not hold exactly the outputs that are asked for");
+    }
+    const Launch l(dev);
+    const int rc = moe_add_rms_norm(
+        xp, dt_code(&x), rp, dt_code(res), wp, dt_code(&w), float_arg(a[3]), as_int(T, "T"),
+        as_int(H, "H"),
+        address(ptr(ro), "residual_out", dev, {res ? res->scalar_type() : at::kBFloat16}, {T, H}),
+        address(ptr(y), "y", dev, {at::kBFloat16}, {T, H}),
+        static_cast<uint8_t*>(address(ptr(codes), "codes", dev, {at::kByte}, {T, H})),
+        static_cast<uint8_t*>(address(ptr(scales), "scales", dev, {at::kByte}, {T, H / 32})),
+        l.stream);
+    return result(rc, {ro, y, codes, scales});
+  });
+}
+
+// (x, w, bias, act, residual, out_f32, ws, out) -> (status, out)
+PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    expect_args(n, 8);
+    const Tensor& x = matrix(a[0], "x");
+    const Tensor& w = matrix(a[1], "w");
+    const Tensor* bias = tensor(a[2], "bias");
+    const int act = static_cast<int>(long_arg(a[3]));
+    const Tensor* res = tensor(a[4], "residual");
+    const int64_t T = x.size(0), K = x.size(1), rows = w.size(0);
+    if (act == MOE_ACT_SWIGLU && rows % 2 != 0)
+      throw ValueError("swiglu needs as many gate rows as up rows, got " + std::to_string(rows) +
+                       " rows");
+    const int64_t N = act == MOE_ACT_SWIGLU ? rows / 2 : rows;
+    const c10::Device dev = x.device();
+    void* xp = address(x, "x", dev, {at::kBFloat16}, {T, K});
+    void* wp = address(w, "w", dev, {at::kBFloat16}, {rows, K});
+    void* bp = address(bias, "bias", dev, {at::kFloat}, {rows});
+    void* rp = address(res, "residual", dev, {at::kBFloat16, at::kFloat}, {T, N});
+    Tensor out;
+    if (a[7] == Py_None)
+      out = at::empty({T, N}, x.options().dtype(bool_arg(a[5]) ? at::kFloat : at::kBFloat16));
+    else
+      out = required(a[7], "out");
+    void* op = address(out, "out", dev, {at::kBFloat16, at::kFloat}, {T, N});
+    const Tensor& ws = required(a[6], "ws");
+    void* wsp = address(ws, "ws", dev, {at::kByte}, {ws.numel()});
+    const Launch l(dev);
+    const int rc =
+        moe_linear(xp, wp, static_cast<float*>(bp), act, rp, dt_code(res), as_int(T, "T"),
+                   as_int(K, "K"), as_int(N, "N"), op, dt_code(&out), wsp, ws.numel(), l.stream);
+    return result(rc, {out});
+  });
+}
+
+struct Balance {
+  const Tensor& logits;
+  int64_t T, E, B = 1;
+  c10::Device dev;
+  void *lp, *mp, *sp;
+  Balance(PyObject* l, PyObject* mask, PyObject* starts)
+      : logits(matrix(l, "logits")), T(logits.size(0)), E(logits.size(1)), dev(logits.device()) {
+    const Tensor* m = tensor(mask, "token_mask");
+    const Tensor* s = tensor(starts, "seq_starts");
+    if (s) {
+      if (s->dim() != 1 || s->numel() < 2)
+        throw ValueError("seq_starts: expected [B + 1], got shape " + shape_text(s->sizes()));
+      B = s->numel() - 1;
+    }
+    lp = address(logits, "logits", dev, {at::kBFloat16, at::kFloat}, {T, E});
+    mp = address(m, "token_mask", dev, {at::kBool, at::kByte}, {T});
+    sp = address(s, "seq_starts", dev, {at::kInt}, {B + 1});
+  }
+};
+
+// (logits, topk_ids, coef, scoring, token_mask, seq_starts, grad, ws, out)
+//   -> (status, loss, counts, tokens, dlogits)
+PyObject* balance_loss(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    expect_args(n, 9);
+    const Balance b(a[0], a[4], a[5]);
+    const Tensor& ids = matrix(a[1], "topk_ids");
+    const int64_t k = ids.size(1);
+    void* ip = address(ids, "topk_ids", b.dev, {at::kInt}, {b.T, k});
+    const bool grad = bool_arg(a[6]);
+    const Tensor& ws = required(a[7], "ws");
+    Tensor loss, counts, tokens, dl;
+    if (a[8] == Py_None) {
+      const auto ints = b.logits.options().dtype(at::kInt);
+      loss = at::empty({1}, b.logits.options().dtype(at::kFloat));
+      counts = at::empty({b.B, b.E}, ints);
+      tokens = at::empty({b.B}, ints);
+      if (grad) dl = at::empty_like(b.logits);
+    } else {
+      loss = out_item(a[8], 4, 0, "loss");
+      counts = out_item(a[8], 4, 1, "counts");
+      tokens = out_item(a[8], 4, 2, "tokens");
+      if (grad) dl = out_item(a[8], 4, 3, "dlogits");
+      if (!loss.defined() || !counts.defined() || !tokens.defined() || grad != dl.defined())
+        throw ValueError("out does not hold the outputs that are asked for");
+    }
+    const Launch l(b.dev);
+    const int rc = moe_balance_loss(
+        b.lp, dt_code(&b.logits), static_cast<int32_t*>(ip), static_cast<uint8_t*>(b.mp),
+        static_cast<int32_t*>(b.sp), as_int(b.B, "B"), as_int(b.T, "T"), as_int(b.E, "E"),
+        as_int(k, "k"), static_cast<int>(long_arg(a[3])), float_arg(a[2]),
+        static_cast<float*>(address(loss, "loss", b.dev, {at::kFloat}, {1})),
+        static_cast<int32_t*>(address(counts, "counts", b.dev, {at::kInt}, {b.B, b.E})),
+        static_cast<int32_t*>(address(tokens, "tokens", b.dev, {at::kInt}, {b.B})),
+        address(ptr(dl), "dlogits", b.dev, {b.logits.scalar_type()}, {b.T, b.E}),
+        address(ws, "ws", b.dev, {at::kByte}, {ws.numel()}), ws.numel(), l.stream);
+    return result(rc, {loss, counts, tokens, dl});
+  });
+}
+
+// (dloss, logits, counts, tokens, coef, scoring, token_mask, seq_starts, out)
+//   -> (status, dlogits)
+PyObject* balance_loss_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    expect_args(n, 9);
+    const Balance b(a[1], a[6], a[7]);
+    void* gp = address(required(a[0], "dloss"), "dloss", b.dev, {at::kFloat}, {1});
+    void* cp = address(required(a[2], "counts"), "counts", b.dev, {at::kInt}, {b.B, b.E});
+    void* tp = address(required(a[3], "tokens"), "tokens", b.dev, {at::kInt}, {b.B});
+    const Tensor out = a[8] == Py_None ? at::empty_like(b.logits) : required(a[8], "dlogits");
+    void* op = address(out, "dlogits", b.dev, {b.logits.scalar_type()}, {b.T, b.E});
+    const Launch l(b.dev);
+    const int rc = moe_balance_loss_backward(
+        static_cast<float*>(gp), b.lp, dt_code(&b.logits), static_cast<int32_t*>(cp),
+        static_cast<int32_t*>(tp), static_cast<uint8_t*>(b.mp), static_cast<int32_t*>(b.sp),
+        as_int(b.B, "B"), as_int(b.T, "T"), as_int(b.E, "E"), static_cast<int>(long_arg(a[5])),
+        float_arg(a[4]), op, l.stream);
+    return result(rc, {out});
+  });
+}
+
+template <class F>
+PyCFunction method(F* f) {
+  return reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(f));
+}
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__moe_bind(void) {
+  static PyMethodDef methods[] = {
+      {"add_rms_norm", method(add_rms_norm), METH_FASTCALL, nullptr},
+      {"linear", method(linear), METH_FASTCALL, nullptr},
+      {"balance_loss", method(balance_loss), METH_FASTCALL, nullptr},
+      {"balance_loss_backward", method(balance_loss_backward), METH_FASTCALL, nullptr},
+      {nullptr, nullptr, 0, nullptr}};
+  static PyModuleDef module = {PyModuleDef_HEAD_INIT, "_moe_bind", nullptr, -1, methods,
+                               nullptr, nullptr, nullptr, nullptr};
+  return PyModule_Create(&module);
+}

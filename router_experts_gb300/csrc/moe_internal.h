@@ -21,7 +21,9 @@ constexpr size_t kWsAlignBarrierOffset = 5120;      // int32[2] grid barrier of 
 constexpr size_t kWsAlignTicketOffset = 5128;       // int32 align: CTAs done reading the counts
 constexpr size_t kWsWaitLimitOffset = 5376;         // int64 test hook: align barrier limit (cycles)
 constexpr size_t kWsDecodeCounterOffset = 6144;     // int32[3] persistent layer: routed, zeroed, done
-constexpr size_t kWsBalanceTicketOffset = 6400;     // int32 balance loss: CTAs done
+constexpr size_t kWsBalanceOffset = 6400;           // int32[5] balance loss: grid barriers, ticket
+constexpr size_t kWsBalancePartOffset = 6528;       // float2[kBalanceMaxSms] CTAs' sums
+constexpr int kBalanceMaxSms = 200;
 constexpr size_t kWsRouterTicketOffset = 8192;      // int32[kRouterMaxTiles]
 constexpr int kRouterMaxTiles = 65536;              // token tiles of 16 -> T <= 1,048,576
 constexpr size_t kWsAlignHistOffset = kWsRouterTicketOffset + 4ull * kRouterMaxTiles;
@@ -194,11 +196,13 @@ int launch_decode_layer(const void* hidden, const void* gate, const float* bias,
                         int num_sms, cudaStream_t stream);
 
 // ---- norm (norm.cu) ---------------------------------------------------------------
-// vec: H % 8 == 0 and every pointer but scales 16-byte aligned.  res may be
+// vec: H % 8 == 0 and every pointer but scales 16-byte aligned.  window: x, res,
+// res_out and y 16-byte aligned, no codes, H % 8 != 0.  res may be
 // nullptr (then res_out is unused); codes need vec and H % 32 == 0.
 int launch_add_rms_norm(const void* x, int x_f32, const void* res, int res_f32, const void* w,
                         int w_f32, float eps, int T, int H, void* res_out, void* y,
-                        uint8_t* codes, uint8_t* scales, bool vec, cudaStream_t stream);
+                        uint8_t* codes, uint8_t* scales, bool vec, bool window,
+                        int num_sms, cudaStream_t stream);
 
 // ---- dense product (linear.cu) ------------------------------------------------------
 enum LinearKind { kLinearToken, kLinearRow, kLinearPair };
@@ -216,21 +220,18 @@ int launch_linear(const void* x, const void* w, const float* bias, int act, cons
                   const char** why);
 
 // ---- balance loss (balance.cu) --------------------------------------------------------
-// CTAs of the token kernel: eight tokens in flight a CTA, four CTAs an SM.
-inline int balance_grid(int T) {
-  const int g = (T + 7) / 8;
-  return g < 608 ? g : 608;
-}
-// vec: E % 4 == 0 and logits / dlogits aligned to four elements.  part:
-// balance_grid(T) doubles; ticket: zero before the first call.
+// vec: E % 4 == 0 and logits / dlogits aligned to four elements.  part: one
+// pair per SM; bars: int32[5], zero before the first call, self-resetting; acc:
+// int32[B * (E + 1)], zero between calls, or nullptr.
 int launch_balance_loss(const void* logits, bool bf16, const int32_t* ids, const uint8_t* mask,
                         const int32_t* starts, int B, int T, int E, int k, int scoring,
                         float coef, float* loss, int32_t* counts, int32_t* tokens, void* dlogits,
-                        bool vec, double* part, int* ticket, int* err, cudaStream_t st);
+                        bool vec, float2* part, int* bars, int* acc, int* err, int num_sms,
+                        cudaStream_t st);
 int launch_balance_loss_backward(const float* dloss, const void* logits, bool bf16,
                                  const int32_t* counts, const int32_t* tokens,
                                  const uint8_t* mask, const int32_t* starts, int B, int T, int E,
-                                 int scoring, float coef, void* dlogits, bool vec,
+                                 int scoring, float coef, void* dlogits, bool vec, int num_sms,
                                  cudaStream_t st);
 
 // ---- floor probes (measurement) -------------------------------------------------

@@ -72,6 +72,50 @@ MOE_DEV void store_f32(float* p, const float (&v)[N]) {
   }
 }
 
+template <int V>
+MOE_DEV void load_weight(const NormArgs& a, int v, float (&w)[V]) {
+  if (a.w_f32) load_f32<V>(static_cast<const float*>(a.w) + v * V, w);
+  else load_bf16<V>(static_cast<const __nv_bfloat16*>(a.w) + v * V, w);
+}
+
+// Every output of vector v of a row that starts at element `row`, from its
+// sums sv; whole warps call it together (`in`: the vector exists).
+template <int V, int RES>
+MOE_DEV void write_vector(const NormArgs& a, size_t row, int v, bool in, float rs,
+                          const float (&sv)[V], const float (&w)[V]) {
+  const size_t at = row + static_cast<size_t>(v) * V;
+  float y[V];
+  if (in) {
+    if constexpr (RES == 1) store_bf16<V>(static_cast<__nv_bfloat16*>(a.res_out) + at, sv);
+    if constexpr (RES == 2) store_f32<V>(static_cast<float*>(a.res_out) + at, sv);
+#pragma unroll
+    for (int i = 0; i < V; ++i) y[i] = sv[i] * rs * w[i];
+    if (a.y) store_bf16<V>(a.y + at, y);
+  }
+  if constexpr (V == 8) {
+    if (a.codes) {
+      // the 32 values of a scale are four neighbouring lanes' (a row's
+      // vectors are a multiple of four, so the four are in or out together)
+      float amax = 0.f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) amax = fmaxf(amax, in ? fabsf(y[i]) : 0.f);
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      if (in) {
+        float mul;
+        const int p = e4m3_scale_exponent(amax, &mul);
+        uint32_t c[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          c[i] = pack_e4m3x4(y[4 * i] * mul, y[4 * i + 1] * mul, y[4 * i + 2] * mul,
+                             y[4 * i + 3] * mul);
+        *reinterpret_cast<uint2*>(a.codes + at) = make_uint2(c[0], c[1]);
+        if ((v & 3) == 0) a.scales[at >> 5] = static_cast<uint8_t>(p + 127);
+      }
+    }
+  }
+}
+
 // V elements per access; IT accesses of each thread cover a row (V = 8) or
 // the row is walked twice (IT = 0, any length).
 template <int V, int IT, bool XF32, int RES>  // RES: 0 none, 1 bf16, 2 f32
@@ -82,6 +126,8 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormArgs a) {
   const int t = blockIdx.x * (blockDim.x / a.group) + g;
   const int nv = a.H / V;
   const bool live = t < a.T;
+  grid_dependency_launch();
+  grid_dependency_wait();
   const size_t row = static_cast<size_t>(live ? t : 0) * a.H;
 
   auto load_s = [&](int v, float (&s)[V]) {
@@ -134,41 +180,9 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormArgs a) {
   const float rs = rsqrtf(sum / static_cast<float>(a.H) + a.eps);
 
   auto finish = [&](int v, float (&sv)[V]) {
-    const bool in = live && v < nv;
-    const size_t at = row + static_cast<size_t>(v) * V;
-    float y[V];
-    if (in) {
-      float w[V];
-      if (a.w_f32) load_f32<V>(static_cast<const float*>(a.w) + v * V, w);
-      else load_bf16<V>(static_cast<const __nv_bfloat16*>(a.w) + v * V, w);
-      if constexpr (RES == 1) store_bf16<V>(static_cast<__nv_bfloat16*>(a.res_out) + at, sv);
-      if constexpr (RES == 2) store_f32<V>(static_cast<float*>(a.res_out) + at, sv);
-#pragma unroll
-      for (int i = 0; i < V; ++i) y[i] = sv[i] * rs * w[i];
-      if (a.y) store_bf16<V>(a.y + at, y);
-    }
-    if constexpr (V == 8) {
-      if (a.codes) {
-        // the 32 values of a scale are four neighbouring lanes' (a row's
-        // vectors are a multiple of four, so the four are in or out together)
-        float amax = 0.f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) amax = fmaxf(amax, in ? fabsf(y[i]) : 0.f);
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        if (in) {
-          float mul;
-          const int p = e4m3_scale_exponent(amax, &mul);
-          uint32_t c[2];
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            c[i] = pack_e4m3x4(y[4 * i] * mul, y[4 * i + 1] * mul, y[4 * i + 2] * mul,
-                               y[4 * i + 3] * mul);
-          *reinterpret_cast<uint2*>(a.codes + at) = make_uint2(c[0], c[1]);
-          if ((v & 3) == 0) a.scales[at >> 5] = static_cast<uint8_t>(p + 127);
-        }
-      }
-    }
+    float w[V];
+    if (live && v < nv) load_weight<V>(a, v, w);
+    write_vector<V, RES>(a, row, v, live && v < nv, rs, sv, w);
   };
   if constexpr (IT > 0) {
 #pragma unroll
@@ -183,25 +197,306 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormArgs a) {
   }
 }
 
-template <int V, int IT>
-void launch_types(const NormArgs& a, int x_f32, int res, int grid, int threads,
-                  cudaStream_t stream) {
-  if (x_f32) {
-    if (res == 0) norm_kernel<V, IT, true, 0><<<grid, threads, 0, stream>>>(a);
-    else if (res == 1) norm_kernel<V, IT, true, 1><<<grid, threads, 0, stream>>>(a);
-    else norm_kernel<V, IT, true, 2><<<grid, threads, 0, stream>>>(a);
-  } else {
-    if (res == 0) norm_kernel<V, IT, false, 0><<<grid, threads, 0, stream>>>(a);
-    else if (res == 1) norm_kernel<V, IT, false, 1><<<grid, threads, 0, stream>>>(a);
-    else norm_kernel<V, IT, false, 2><<<grid, threads, 0, stream>>>(a);
+// Many rows: each CTA (two an SM where the ring fits) walks rows blockIdx.x +
+// i gridDim.x with `group` threads, IT vectors of 8 a thread; the rows of x and
+// residual come by bulk copies into a ring of `depth` stages, so that about
+// 200 KB an SM are in flight, and the weights stay in registers.  With one
+// row in flight a CTA the same rows moved at 4.5 TB/s.
+template <int IT, bool XF32, int RES>
+__global__ void __launch_bounds__(1024) norm_rows_kernel(const NormArgs a, int depth, int* err) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t full[8];
+  __shared__ float part[2][32];
+  __shared__ int abort_flag;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int nv = a.H / 8, warps = blockDim.x >> 5;
+  const uint32_t xb = a.H * (XF32 ? 4u : 2u), rb = a.H * (RES == 0 ? 0u : RES == 1 ? 2u : 4u);
+  auto load_row = [&](int st, int t) {
+    uint8_t* dst = smem + st * (xb + rb);
+    mbar_arrive_expect_tx(&full[st], xb + rb);
+    bulk_load(dst, static_cast<const char*>(a.x) + static_cast<size_t>(t) * xb, xb, &full[st]);
+    if (RES != 0)
+      bulk_load(dst + xb, static_cast<const char*>(a.res) + static_cast<size_t>(t) * rb, rb,
+                &full[st]);
+  };
+  grid_dependency_launch();
+  if (tid == 0) {
+    for (int i = 0; i < depth; ++i) mbar_init(&full[i], 1);
+    abort_flag = 0;
+    mbar_fence_init();
+    fence_proxy_async_smem();
+    grid_dependency_wait();
+    for (int i = 0; i < depth; ++i) {
+      const long long t = blockIdx.x + static_cast<long long>(i) * gridDim.x;
+      if (t < a.T) load_row(i, static_cast<int>(t));
+    }
   }
+  grid_dependency_wait();
+  float w[IT][8];
+#pragma unroll
+  for (int k = 0; k < IT; ++k) {
+    const int v = tid + k * blockDim.x;
+    if (v < nv) load_weight<8>(a, v, w[k]);
+  }
+  __syncthreads();
+  int st = 0, buf = 0;
+  uint32_t ph = 0;
+  for (long long t = blockIdx.x; t < a.T; t += gridDim.x) {
+    const bool ok = mbar_wait(&full[st], ph, &abort_flag, err);
+    const uint8_t* src = smem + st * (xb + rb);
+    float s[IT][8];
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < IT; ++k) {
+      const int v = tid + k * blockDim.x;
+      if (v < nv) {
+        if constexpr (XF32) load_f32<8>(reinterpret_cast<const float*>(src) + v * 8, s[k]);
+        else load_bf16<8>(reinterpret_cast<const __nv_bfloat16*>(src) + v * 8, s[k]);
+        if constexpr (RES != 0) {
+          float q[8];
+          if constexpr (RES == 2) load_f32<8>(reinterpret_cast<const float*>(src + xb) + v * 8, q);
+          else load_bf16<8>(reinterpret_cast<const __nv_bfloat16*>(src + xb) + v * 8, q);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) s[k][i] += q[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum = fmaf(s[k][i], s[k][i], sum);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[k][i] = 0.f;
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) part[buf][warp] = sum;
+    if (__syncthreads_or(!ok)) return;  // (also: every thread has read the stage)
+    if (tid == 0) {
+      const long long next = t + static_cast<long long>(depth) * gridDim.x;
+      if (next < a.T) load_row(st, static_cast<int>(next));
+    }
+    sum = lane < warps ? part[buf][lane] : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const float rs = rsqrtf(sum / static_cast<float>(a.H) + a.eps);
+#pragma unroll
+    for (int k = 0; k < IT; ++k) {
+      const int v = tid + k * blockDim.x;
+      write_vector<8, RES>(a, static_cast<size_t>(t) * a.H, v, v < nv, rs, s[k], w[k]);
+    }
+    buf ^= 1;
+    if (++st == depth) st = 0, ph ^= 1;
+  }
+}
+
+template <class Kernel, class... Args>
+int launch_dependent(Kernel kernel, int grid, int threads, int smem, cudaStream_t stream,
+                     Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) return -1;
+  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+}
+
+template <int IT, bool XF32, int RES>
+int launch_rows(const NormArgs& a, int threads, int depth, int smem, int grid, int* err,
+                cudaStream_t stream) {
+  static std::atomic<unsigned long long> smem_set{0};
+  const auto kernel = norm_rows_kernel<IT, XF32, RES>;
+  if (!ensure_smem_limit(reinterpret_cast<const void*>(kernel), 220 * 1024, smem_set)) return -1;
+  return launch_dependent(kernel, grid, threads, smem, stream, a, depth, err);
+}
+template <int IT>
+int launch_rows_types(const NormArgs& a, int x_f32, int res, int threads, int depth, int smem,
+                      int grid, int* err, cudaStream_t st) {
+  if (x_f32)
+    return res == 0   ? launch_rows<IT, true, 0>(a, threads, depth, smem, grid, err, st)
+           : res == 1 ? launch_rows<IT, true, 1>(a, threads, depth, smem, grid, err, st)
+                      : launch_rows<IT, true, 2>(a, threads, depth, smem, grid, err, st);
+  return res == 0   ? launch_rows<IT, false, 0>(a, threads, depth, smem, grid, err, st)
+         : res == 1 ? launch_rows<IT, false, 1>(a, threads, depth, smem, grid, err, st)
+                    : launch_rows<IT, false, 2>(a, threads, depth, smem, grid, err, st);
+}
+
+// Rows whose start is no 16-byte boundary (H % 8 != 0 on aligned bases): the
+// tensors are still walked in aligned vectors of 8, of which a row owns all but
+// the ends of its first and last one; only those are stored by elements.  x,
+// residual and the outputs share the row's shift against the vectors, so only
+// the weights need another one: they sit in shared memory as floats, one gap
+// in eight, which spreads the lanes' reads at a stride of 8 over all banks.
+// Element by element, 1021 x 2045 took 7.1 us.
+template <int IT, bool XF32, int RES>
+__global__ void __launch_bounds__(IT == 1 ? 256 : 1024) norm_window_kernel(const NormArgs a) {
+  extern __shared__ __align__(16) float wsm[];
+  __shared__ float part[2][32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+  grid_dependency_launch();
+  grid_dependency_wait();
+  const size_t total = static_cast<size_t>(a.T) * a.H;
+  // sums of the IT vectors of row t; elements [lo, hi) of a vector are the row's
+  auto bounds = [&](size_t row, int v, int* lo, int* hi) {
+    const int j = 8 * v - static_cast<int>(row & 7);
+    *lo = max(0, -j);
+    *hi = min(8, a.H - j);
+  };
+  auto load = [&](long long t, float (&s)[IT][8]) {
+    const size_t row = static_cast<size_t>(t) * a.H;
+#pragma unroll
+    for (int k = 0; k < IT; ++k) {
+      const int v = tid + k * blockDim.x;
+      int lo, hi;
+      bounds(row, v, &lo, &hi);
+      const size_t at = (row & ~size_t{7}) + 8 * static_cast<size_t>(v);
+      // whole vectors also where a neighbouring row owns a part (a branch of
+      // its own for the ends would wait for memory twice); only what reaches
+      // past the tensor goes by elements
+      if (at + 8 <= total) {
+        if (hi > lo) {
+          if constexpr (XF32) load_f32<8>(static_cast<const float*>(a.x) + at, s[k]);
+          else load_bf16<8>(static_cast<const __nv_bfloat16*>(a.x) + at, s[k]);
+          if constexpr (RES != 0) {
+            float q[8];
+            if constexpr (RES == 2) load_f32<8>(static_cast<const float*>(a.res) + at, q);
+            else load_bf16<8>(static_cast<const __nv_bfloat16*>(a.res) + at, q);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s[k][i] += q[i];
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float v1 = 0.f;
+          if (i >= lo && i < hi) {
+            v1 = XF32 ? static_cast<const float*>(a.x)[at + i]
+                      : __bfloat162float(static_cast<const __nv_bfloat16*>(a.x)[at + i]);
+            if constexpr (RES == 1)
+              v1 += __bfloat162float(static_cast<const __nv_bfloat16*>(a.res)[at + i]);
+            if constexpr (RES == 2) v1 += static_cast<const float*>(a.res)[at + i];
+          }
+          s[k][i] = v1;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[k][i] = i >= lo && i < hi ? s[k][i] : 0.f;
+    }
+  };
+  float s[IT][8];
+  load(blockIdx.x, s);
+  {  // the weights, four loads of a thread at a time
+    for (int i0 = tid; i0 < a.H; i0 += 4 * blockDim.x) {
+      float w[4][1];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (i0 + u * blockDim.x < a.H) load_weight<1>(a, i0 + u * blockDim.x, w[u]);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int k = i0 + u * blockDim.x + 8;
+        if (k < a.H + 8) wsm[k + (k >> 3)] = w[u][0];
+      }
+    }
+  }
+  __syncthreads();
+  int buf = 0;
+  for (long long t = blockIdx.x; t < a.T; t += gridDim.x) {
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < IT; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum = fmaf(s[k][i], s[k][i], sum);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) part[buf][warp] = sum;
+    // the next row is in flight while this one is finished
+    float next[IT][8];
+    if (t + gridDim.x < a.T) load(t + gridDim.x, next);
+    __syncthreads();
+    sum = lane < warps ? part[buf][lane] : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const float rs = rsqrtf(sum / static_cast<float>(a.H) + a.eps);
+    buf ^= 1;
+    const size_t row = static_cast<size_t>(t) * a.H;
+    const int shift = static_cast<int>(row & 7);
+#pragma unroll
+    for (int k = 0; k < IT; ++k) {
+      const int v = tid + k * blockDim.x;
+      int lo, hi;
+      bounds(row, v, &lo, &hi);
+      const size_t at = row - shift + 8 * static_cast<size_t>(v);
+      if (lo == 0 && hi == 8) {
+        float y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int q = 8 * (v + 1) - shift + i;
+          y[i] = s[k][i] * rs * wsm[q + (q >> 3)];
+        }
+        if constexpr (RES == 1) store_bf16<8>(static_cast<__nv_bfloat16*>(a.res_out) + at, s[k]);
+        if constexpr (RES == 2) store_f32<8>(static_cast<float*>(a.res_out) + at, s[k]);
+        store_bf16<8>(a.y + at, y);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (i >= lo && i < hi) {
+            const int q = 8 * (v + 1) - shift + i;
+            if constexpr (RES == 1)
+              static_cast<__nv_bfloat16*>(a.res_out)[at + i] = __float2bfloat16_rn(s[k][i]);
+            if constexpr (RES == 2) static_cast<float*>(a.res_out)[at + i] = s[k][i];
+            a.y[at + i] = __float2bfloat16_rn(s[k][i] * rs * wsm[q + (q >> 3)]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < IT; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[k][i] = next[k][i];
+  }
+}
+
+template <int IT, bool XF32, int RES>
+int launch_window(const NormArgs& a, int threads, int smem, int grid, cudaStream_t stream) {
+  static std::atomic<unsigned long long> smem_set{0};
+  const auto kernel = norm_window_kernel<IT, XF32, RES>;
+  if (!ensure_smem_limit(reinterpret_cast<const void*>(kernel), 80 * 1024, smem_set)) return -1;
+  return launch_dependent(kernel, grid, threads, smem, stream, a);
+}
+template <int IT>
+int launch_window_types(const NormArgs& a, int x_f32, int res, int threads, int smem, int grid,
+                        cudaStream_t st) {
+  if (x_f32)
+    return res == 0   ? launch_window<IT, true, 0>(a, threads, smem, grid, st)
+           : res == 1 ? launch_window<IT, true, 1>(a, threads, smem, grid, st)
+                      : launch_window<IT, true, 2>(a, threads, smem, grid, st);
+  return res == 0   ? launch_window<IT, false, 0>(a, threads, smem, grid, st)
+         : res == 1 ? launch_window<IT, false, 1>(a, threads, smem, grid, st)
+                    : launch_window<IT, false, 2>(a, threads, smem, grid, st);
+}
+
+template <int V, int IT>
+int launch_types(const NormArgs& a, int x_f32, int res, int grid, int threads,
+                 cudaStream_t st) {
+  if (x_f32)
+    return res == 0   ? launch_dependent(norm_kernel<V, IT, true, 0>, grid, threads, 0, st, a)
+           : res == 1 ? launch_dependent(norm_kernel<V, IT, true, 1>, grid, threads, 0, st, a)
+                      : launch_dependent(norm_kernel<V, IT, true, 2>, grid, threads, 0, st, a);
+  return res == 0   ? launch_dependent(norm_kernel<V, IT, false, 0>, grid, threads, 0, st, a)
+         : res == 1 ? launch_dependent(norm_kernel<V, IT, false, 1>, grid, threads, 0, st, a)
+                    : launch_dependent(norm_kernel<V, IT, false, 2>, grid, threads, 0, st, a);
 }
 
 }  // namespace
 
 int launch_add_rms_norm(const void* x, int x_f32, const void* res, int res_f32, const void* w,
                         int w_f32, float eps, int T, int H, void* res_out, void* y,
-                        uint8_t* codes, uint8_t* scales, bool vec, cudaStream_t stream) {
+                        uint8_t* codes, uint8_t* scales, bool vec, bool window,
+                        int num_sms, cudaStream_t stream) {
   NormArgs a{};
   a.x = x;
   a.res = res;
@@ -217,6 +512,35 @@ int launch_add_rms_norm(const void* x, int x_f32, const void* res, int res_f32, 
   const int r = res ? (res_f32 ? 2 : 1) : 0;
   const int V = vec ? 8 : 1;
   const int nv = H / V;
+  if (window) {
+    const int n = H / 8 + 2;  // vectors that a row may touch
+    const int it = n <= 256 ? 1 : n <= 2048 ? 2 : 0;
+    const int threads = it ? ((n + it - 1) / it + 31) / 32 * 32 : 0;
+    const int smem = (H + 16) * 9 / 8 * 4 + 16;
+    if (it && H >= 128) {
+      const int per_sm = threads <= 640 ? 1280 / threads : 1;
+      const int grid = T < per_sm * num_sms ? T : per_sm * num_sms;
+      return it == 1 ? launch_window_types<1>(a, x_f32, r, threads, smem, grid, stream)
+                     : launch_window_types<2>(a, x_f32, r, threads, smem, grid, stream);
+    }
+  }
+  if (vec) {
+    // rows of 4 KB or more, at least two for every CTA of the ring kernel
+    const int stage = H * ((x_f32 ? 4 : 2) + (r == 0 ? 0 : r == 1 ? 2 : 4));
+    const int it = nv <= 512 ? 1 : nv <= 2048 ? 2 : 4;
+    const int threads = ((nv + it - 1) / it + 31) / 32 * 32;
+    // as many CTAs as about 1024 threads and two stages each let on an SM
+    int ctas = 1024 / threads;
+    while (ctas > 1 && ctas * 2 * stage > 220 * 1024) --ctas;
+    int depth = ctas > 0 ? 220 * 1024 / ctas / stage : 0;
+    if (depth > 4) depth = 4;
+    if (stage >= 4096 && threads <= 1024 && depth >= 2 && T >= 2 * ctas * num_sms) {
+      const int smem = depth * stage, grid = ctas * num_sms;
+      return it == 1   ? launch_rows_types<1>(a, x_f32, r, threads, depth, smem, grid, nullptr, stream)
+             : it == 2 ? launch_rows_types<2>(a, x_f32, r, threads, depth, smem, grid, nullptr, stream)
+                       : launch_rows_types<4>(a, x_f32, r, threads, depth, smem, grid, nullptr, stream);
+    }
+  }
   // threads of a row: at most two 16-byte (eight scalar) accesses a thread
   const int per = vec ? 2 : 8;
   int group = ((nv + per - 1) / per + 31) / 32 * 32;
@@ -225,15 +549,12 @@ int launch_add_rms_norm(const void* x, int x_f32, const void* res, int res_f32, 
   const int rows = group >= 256 ? 1 : 256 / group;
   const int grid = (T + rows - 1) / rows;
   const int threads = rows * group;
-  if (vec) {
-    if (nv <= 2 * group) launch_types<8, 2>(a, x_f32, r, grid, threads, stream);
-    else if (nv <= 4 * group) launch_types<8, 4>(a, x_f32, r, grid, threads, stream);
-    else launch_types<8, 0>(a, x_f32, r, grid, threads, stream);
-  } else {
-    if (nv <= 8 * group) launch_types<1, 8>(a, x_f32, r, grid, threads, stream);
-    else launch_types<1, 0>(a, x_f32, r, grid, threads, stream);
-  }
-  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+  if (vec)
+    return nv <= 2 * group   ? launch_types<8, 2>(a, x_f32, r, grid, threads, stream)
+           : nv <= 4 * group ? launch_types<8, 4>(a, x_f32, r, grid, threads, stream)
+                             : launch_types<8, 0>(a, x_f32, r, grid, threads, stream);
+  return nv <= 8 * group ? launch_types<1, 8>(a, x_f32, r, grid, threads, stream)
+                         : launch_types<1, 0>(a, x_f32, r, grid, threads, stream);
 }
 
 }  // namespace moe

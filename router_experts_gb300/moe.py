@@ -1,4 +1,5 @@
-"""Python binding of the C ABI in ``include/moe.h`` (argument marshalling only).
+"""Python binding of the C ABI in ``include/moe.h`` (argument marshalling only;
+part of it native, ``csrc/bind.cpp``).
 
 Every step runs in the CUDA library ``libmoe.so``; this module passes torch
 tensors' device pointers and sizes through ctypes and raises on any non-zero
@@ -7,6 +8,7 @@ status.  There is no fallback: if the library is not built, every call raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 
@@ -14,6 +16,7 @@ import torch
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "_build", "libmoe.so")
+BIND_PATH = os.path.join(HERE, "_build", "_moe_bind.so")
 
 MOE_OK, MOE_ERR_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA, MOE_ERR_DEVICE = 0, 1, 2, 3, 4
 SOFTMAX, SIGMOID, SQRT_SOFTPLUS = 0, 1, 2
@@ -407,35 +410,38 @@ def layer_persistent(hidden, gate, bias, w13, w2, k, scoring="softmax", n_group=
 
 
 # ---- operators around the layer ----------------------------------------------------
+# Their checks of tensors and the marshalling are native (csrc/bind.cpp): for one
+# token they cost more than the kernels when done here.
 
-_FLOAT_DT = {torch.bfloat16: DT_BF16, torch.float32: DT_F32}
-
-
-def _arg(name, t, shape, dtypes, device):
-    """Device address of a tensor argument after the checks that keep the
-    kernels inside it: device, type, shape, dense layout.  None passes."""
-    if t is None:
-        return None
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{name}: expected a CUDA tensor on {device}, got one on {t.device}")
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name}: unsupported dtype {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous tensor, got strides {t.stride()}")
-    return t.data_ptr()
+_bind = None
+_bind_ws_bytes = 0
 
 
-_BF16, _F32, _I32 = (torch.bfloat16,), (torch.float32,), (torch.int32,)
-_U8, _MASK = (torch.uint8,), (torch.bool, torch.uint8)
-_FLOATS = (torch.bfloat16, torch.float32)
+def _native():
+    """The native part of the binding (raises if it has not been built)."""
+    global _bind, _bind_ws_bytes
+    if _bind is None:
+        lib = load()
+        if not os.path.exists(BIND_PATH):
+            raise RuntimeError(f"native binding not built: {BIND_PATH} is missing "
+                               "(run router_experts_gb300.build.build())")
+        spec = importlib.util.spec_from_file_location("_moe_bind", BIND_PATH)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+        # one size serves every call of these operators
+        _bind_ws_bytes = max(lib.moe_linear_workspace_bytes(1, 8, 1, 0),
+                             lib.moe_balance_loss_workspace_bytes(1, 512, 65536))
+        _bind = mod
+    return _bind
 
 
-def _shape2(name, t):
-    if t.dim() != 2:
-        raise ValueError(f"{name}: expected a matrix, got shape {tuple(t.shape)}")
-    return t.shape
+def _operator_ws(ws, t):
+    dev = t.device
+    if dev.type != "cuda":
+        return None  # refused by the native checks
+    ws = ws or _default_ws.get(("cuda", dev.index)) or default_workspace(dev)
+    buf = ws.buf
+    return buf if buf is not None and buf.numel() >= _bind_ws_bytes else ws.get(_bind_ws_bytes)
 
 
 def add_rms_norm(x, weight, residual=None, eps=1e-6, y=True, e4m3=False, out=None):
@@ -447,31 +453,9 @@ def add_rms_norm(x, weight, residual=None, eps=1e-6, y=True, e4m3=False, out=Non
     and hidden_scale).  -> (residual_out, y, codes, scales), None for what was
     not asked for.  out: the same four, to write into; residual_out may be
     residual itself."""
-    T, H = _shape2("x", x)
-    dev = x.device
-    if not y and not e4m3:
-        raise ValueError("nothing to write: y and e4m3 are both False")
-    if e4m3 and H % 32 != 0:
-        raise ValueError(f"e4m3 needs whole groups of 32 values, got rows of {H}")
-    if out is None:
-        out = (torch.empty_like(residual) if residual is not None else None,
-               torch.empty((T, H), dtype=torch.bfloat16, device=dev) if y else None,
-               torch.empty((T, H), dtype=torch.uint8, device=dev) if e4m3 else None,
-               torch.empty((T, H // 32), dtype=torch.uint8, device=dev) if e4m3 else None)
-    ro, yo, codes, scales = out
-    if (residual is None) != (ro is None) or y != (yo is not None) or \
-            e4m3 != (codes is not None) or e4m3 != (scales is not None):
-        raise ValueError("out does not hold exactly the outputs that are asked for")
-    rdt = residual.dtype if residual is not None else torch.bfloat16
-    shape = x.shape
-    rc = load().moe_add_rms_norm(
-        _arg("x", x, shape, _FLOATS, dev), _FLOAT_DT[x.dtype],
-        _arg("residual", residual, shape, _FLOATS, dev), _FLOAT_DT.get(rdt, -1),
-        _arg("weight", weight, (H,), _FLOATS, dev), _FLOAT_DT[weight.dtype], eps, T, H,
-        _arg("residual_out", ro, shape, (rdt,), dev), _arg("y", yo, shape, _BF16, dev),
-        _arg("codes", codes, shape, _U8, dev), _arg("scales", scales, (T, H // 32), _U8, dev),
-        torch.cuda.current_stream(dev).cuda_stream)
-    _check(rc, "moe_add_rms_norm")
+    rc, ro, yo, codes, scales = _native().add_rms_norm(x, weight, residual, eps, y, e4m3, out)
+    if rc:
+        _check(rc, "moe_add_rms_norm")
     return ro, yo, codes, scales
 
 
@@ -486,41 +470,18 @@ def linear(x, w, bias=None, activation=None, residual=None, out_dtype=torch.bflo
     x [T, K] bf16, w [N, K] bf16; activation None, "silu", "gelu" or "swiglu"
     (then w is [2N, K]: gate rows first, then up rows); bias f32 with one value
     a row of w; residual [T, N] bf16 or f32.  K % 8 == 0."""
-    lib = load()
-    T, K = _shape2("x", x)
-    rows = _shape2("w", w)[0]
-    dev = x.device
-    act = ACTIVATIONS[activation]
-    if act == 3 and rows % 2 != 0:
-        raise ValueError(f"swiglu needs as many gate rows as up rows, got {rows} rows")
-    N = rows // 2 if act == 3 else rows
-    if out is None:
-        out = torch.empty((T, N), dtype=out_dtype, device=dev)
-    need = lib.moe_linear_workspace_bytes(T, K, N, act)
-    buf = (ws or default_workspace(dev)).get(need) if dev.type == "cuda" else None
-    rdt = residual.dtype if residual is not None else torch.bfloat16
-    rc = lib.moe_linear(
-        _arg("x", x, (T, K), _BF16, dev), _arg("w", w, (rows, K), _BF16, dev),
-        _arg("bias", bias, (rows,), _F32, dev), act,
-        _arg("residual", residual, (T, N), _FLOATS, dev), _FLOAT_DT.get(rdt, -1), T, K, N,
-        _arg("out", out, (T, N), _FLOATS, dev), _FLOAT_DT[out.dtype],
-        _p(buf), buf.numel() if buf is not None else 0,
-        torch.cuda.current_stream(dev).cuda_stream)
-    _check(rc, "moe_linear")
+    if out is None and out_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"out_dtype: unsupported dtype {out_dtype}")
+    bind = _native()
+    rc, out = bind.linear(x, w, bias, ACTIVATIONS[activation], residual,
+                          out_dtype is torch.float32, _operator_ws(ws, x), out)
+    if rc:
+        _check(rc, "moe_linear")
     return out
 
 
-def _balance_args(logits, scoring, token_mask, seq_starts):
-    T, E = _shape2("logits", logits)
-    dev = logits.device
-    B = 1
-    if seq_starts is not None:
-        if seq_starts.dim() != 1 or seq_starts.numel() < 2:
-            raise ValueError(f"seq_starts: expected [B + 1], got {tuple(seq_starts.shape)}")
-        B = seq_starts.numel() - 1
-    return (T, E, B, dev, _arg("logits", logits, (T, E), _FLOATS, dev),
-            _arg("token_mask", token_mask, (T,), _MASK, dev),
-            _arg("seq_starts", seq_starts, (B + 1,), _I32, dev), SCORING[scoring])
+def balance_loss_workspace_bytes(T, E, B=1) -> int:
+    return int(load().moe_balance_loss_workspace_bytes(T, E, B))
 
 
 def balance_loss(logits, topk_ids, coef, scoring="softmax", token_mask=None, seq_starts=None,
@@ -532,42 +493,23 @@ def balance_loss(logits, topk_ids, coef, scoring="softmax", token_mask=None, seq
     token_mask [T] (zero: padding, not counted); seq_starts [B+1] int32: the
     loss is the mean over the sequences (B = 1 without).  grad=True also writes
     the gradient of the loss: `logits.backward(dlogits)`, or add it to that of
-    other terms; balance_loss_backward makes it later, times an outer gradient."""
-    lib = load()
-    T, E, B, dev, lp, mp, sp, sc = _balance_args(logits, scoring, token_mask, seq_starts)
-    k = _shape2("topk_ids", topk_ids)[1]
-    if out is None:
-        out = (torch.empty(1, dtype=torch.float32, device=dev),
-               torch.empty((B, E), dtype=torch.int32, device=dev),
-               torch.empty(B, dtype=torch.int32, device=dev),
-               torch.empty_like(logits) if grad else None)
-    loss, counts, tokens, dl = out
-    if not grad:
-        dl = None
-    elif dl is None:
-        raise ValueError("out has no dlogits, and grad is True")
-    need = lib.moe_balance_loss_workspace_bytes(T, E, B)
-    buf = (ws or default_workspace(dev)).get(need)
-    rc = lib.moe_balance_loss(
-        lp, _FLOAT_DT[logits.dtype], _arg("topk_ids", topk_ids, (T, k), _I32, dev), mp, sp, B, T,
-        E, k, sc, coef, _arg("loss", loss, (1,), _F32, dev),
-        _arg("counts", counts, (B, E), _I32, dev), _arg("tokens", tokens, (B,), _I32, dev),
-        _arg("dlogits", dl, (T, E), (logits.dtype,), dev), _p(buf), buf.numel(),
-        torch.cuda.current_stream(dev).cuda_stream)
-    _check(rc, "moe_balance_loss")
-    return loss, counts, tokens, dl
+    other terms; balance_loss_backward makes it later, times an outer gradient.
+    out: the same four, to write into (dlogits is left alone without grad)."""
+    bind = _native()
+    rc, loss, counts, tokens, dlogits = bind.balance_loss(
+        logits, topk_ids, coef, SCORING[scoring], token_mask, seq_starts, grad,
+        _operator_ws(ws, logits), out)
+    if rc:
+        _check(rc, "moe_balance_loss")
+    return loss, counts, tokens, dlogits
 
 
 def balance_loss_backward(dloss, logits, counts, tokens, coef, scoring="softmax",
                           token_mask=None, seq_starts=None, out=None):
     """dlogits = dloss * d balance_loss / d logits, from the counts and tokens
     that balance_loss gave for the same arguments; dloss [1] f32 on the device."""
-    T, E, B, dev, lp, mp, sp, sc = _balance_args(logits, scoring, token_mask, seq_starts)
-    out = torch.empty_like(logits) if out is None else out
-    rc = load().moe_balance_loss_backward(
-        _arg("dloss", dloss, (1,), _F32, dev), lp, _FLOAT_DT[logits.dtype],
-        _arg("counts", counts, (B, E), _I32, dev), _arg("tokens", tokens, (B,), _I32, dev), mp,
-        sp, B, T, E, sc, coef, _arg("dlogits", out, (T, E), (logits.dtype,), dev),
-        torch.cuda.current_stream(dev).cuda_stream)
-    _check(rc, "moe_balance_loss_backward")
+    rc, out = _native().balance_loss_backward(dloss, logits, counts, tokens, coef,
+                                              SCORING[scoring], token_mask, seq_starts, out)
+    if rc:
+        _check(rc, "moe_balance_loss_backward")
     return out

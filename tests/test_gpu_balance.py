@@ -3,8 +3,8 @@
 Tolerances.  Counts are whole numbers: equal.  A probability takes an
 exponential, a root or a reciprocal (each good to a few 2^-24) and a sum of at
 most 512 scores in 32 bits (16 of a lane one after the other, then a tree): 2^-19
-relative is more than twice their sum.  The loss adds tokens in 64 bits:
-2^-18.  In the gradient c d (g_e - sum g p) each part has that error:
+relative is more than twice their sum.  The loss adds tokens in pairs of
+floats: 2^-18.  In the gradient c d (g_e - sum g p) each part has that error:
 2^-18 c d (|g_e| + sum |g| p), and one rounding to the logits' type."""
 import pytest
 import torch
