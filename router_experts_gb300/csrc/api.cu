@@ -643,7 +643,7 @@ int moe_linear(const void* x, const void* w, const float* bias, int act, const v
     return MOE_ERR_ARG;
   const int sms = device_num_sms();
   if (sms <= 0) return cuda_fail("cudaDeviceGetAttribute", cudaGetLastError());
-  const LinearPlan plan = plan_linear(T, K, N, act == MOE_ACT_SWIGLU, sms);
+  const LinearPlan plan = plan_linear(T, K, N, act == MOE_ACT_SWIGLU, out_dt == MOE_DT_F32, sms);
   const char* why = "";
   if (launch_linear(x, w, bias, act, residual, residual_dt == MOE_DT_F32, T, K, N, out,
                     out_dt == MOE_DT_F32, plan, err_word(ws), sms, static_cast<cudaStream_t>(stream),

@@ -21,6 +21,11 @@
 // of it into the owner's shared memory, and the owner adds them in split
 // order and runs the epilogue.  No partial goes through HBM, nothing spins,
 // and the same inputs give the same bits.
+//
+// The tensor core cuts its running sum off towards zero at every step: a chain
+// of 8192 terms ends 9e-6 low (2-norm, relative), of 512 terms 5e-7.  That
+// vanishes in a bf16 output; for 32-bit outputs no chain is longer than about
+// kChain K steps, and the pieces are added in registers with rounding.
 #include "moe_common.cuh"
 #include "moe_internal.h"
 
@@ -30,7 +35,8 @@ namespace moe {
 
 namespace {
 
-constexpr int kBK = 64;  // K elements of a stage (128 bytes of bf16)
+constexpr int kBK = 64;    // K elements of a stage (128 bytes of bf16)
+constexpr int kChain = 8;  // K steps of a tensor-core sum of a 32-bit output
 
 struct LinearArgs {
   const float* bias;
@@ -249,7 +255,8 @@ struct RowCfg {
   static constexpr int STAGE_BYTES = A_BYTES + BN * 128;
   static constexpr int RECV_BYTES = BN * 128 * 4;
   static constexpr int STAGES = BN == 64 ? 3 : 4;
-  static constexpr int TMEM_COLS = BN;
+  static constexpr int PIECES = BN == 32 ? 8 : 4;  // accumulators of a chain's pieces
+  static constexpr int TMEM_COLS = PIECES * BN;    // two CTAs share an SM's 512 (BN <= 64)
   static constexpr int THREADS = 192;
   static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + RECV_BYTES + 1024 + 256;
   static_assert(SMEM_BYTES <= (BN == 128 ? 232448 : 232448 / 2 - 1024), "shared memory budget");
@@ -280,6 +287,9 @@ __global__ void __launch_bounds__(RowCfg<BN>::THREADS)
   const int KB = (a.K + kBK - 1) / kBK;
   int kb0, kb1;
   split_range(KB, S, s, &kb0, &kb1);
+  // the chain in pieces of whole steps, each with its own accumulator
+  const int piece = (kb1 - kb0 + C::PIECES - 1) / C::PIECES;
+  const int pieces = (kb1 - kb0 + piece - 1) / piece;
 
   grid_dependency_launch();
   // one lane: the copies of K step kb into stage st
@@ -329,8 +339,8 @@ __global__ void __launch_bounds__(RowCfg<BN>::THREADS)
   } else if (warp == 1) {
     const uint64_t desc0 = sw128_desc(smem_u32(smem));
     bool alive = true;
-    int st = 0;
-    uint32_t ph = 0;
+    int st = 0, left = piece;
+    uint32_t ph = 0, d = tmem_base, acc = 0;
     for (int kb = kb0; kb < kb1; ++kb) {
       if (!mbar_wait(&full_bar[st], ph, abort_flag, a.err)) {
         alive = false;
@@ -341,11 +351,13 @@ __global__ void __launch_bounds__(RowCfg<BN>::THREADS)
       if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < kBK / 16; ++kk)
-          umma_f16(tmem_base, da + 2 * kk, da + (C::A_BYTES >> 4) + 2 * kk,
-                   idesc_bf16_f32(128, BN), (kb > kb0 || kk > 0) ? 1u : 0u);
+          umma_f16(d, da + 2 * kk, da + (C::A_BYTES >> 4) + 2 * kk, idesc_bf16_f32(128, BN),
+                   kk > 0 ? 1u : acc);
         umma_commit(&empty_bar[st]);
       }
       __syncwarp();
+      acc = 1;
+      if (--left == 0) left = piece, d += BN, acc = 0;
       if (++st == C::STAGES) st = 0, ph ^= 1;
     }
     if (alive && elect_one()) umma_commit(done_bar);
@@ -406,10 +418,20 @@ __global__ void __launch_bounds__(RowCfg<BN>::THREADS)
       const float* to = recv + s * P * 128 + row * 4;
 #pragma unroll 1
       for (int c0 = 0; c0 < cols; c0 += 16) {
+        const uint32_t tb = tmem_base + (static_cast<uint32_t>(ew * 32) << 16) + c0;
         uint32_t v[16];
-        tmem_ld16(tmem_base + (static_cast<uint32_t>(ew * 32) << 16) + c0, v);
+        tmem_ld16(tb, v);
         tmem_ld_wait();
         reg_fence16(v);
+        for (int p = 1; p < pieces; ++p) {
+          uint32_t w[16];
+          tmem_ld16(tb + p * BN, w);
+          tmem_ld_wait();
+          reg_fence16(w);
+#pragma unroll
+          for (int c = 0; c < 16; ++c)
+            v[c] = __float_as_uint(__uint_as_float(v[c]) + __uint_as_float(w[c]));
+        }
 #pragma unroll
         for (int c = 0; c < 16; c += U) {
           const int q = (c0 + c) >> lp;  // P >= 4 and a power of two
@@ -488,6 +510,9 @@ __global__ void __launch_bounds__(RowCfg<BN>::THREADS)
 //                  one tile overlaps the MMAs of the next
 //   SPLIT = true:  one tile per cluster of `splits` pairs, each a part of K;
 //                  the ring is the receive buffer once its MMAs are done
+//   WIDE = true (32-bit outputs, not split): the accumulators turn every kChain
+//                  K steps and the epilogue adds them up in registers, which
+//                  hold bn <= 160 columns (gated 128)
 //   warp 0     TMA producer      warp 1    TMEM allocation, MMA issue
 //   warps 2-9  epilogue, two per TMEM lane quarter
 // ---------------------------------------------------------------------------
@@ -636,7 +661,7 @@ MOE_DEV void chunk_loop(const LinearArgs& a, int trow0, int n0, int first, int e
   }
 }
 
-template <int ACT, bool VEC, bool SPLIT>
+template <int ACT, bool VEC, bool SPLIT, bool WIDE>
 __global__ void __launch_bounds__(kPairThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap tm_w,
                        const __grid_constant__ CUtensorMap tm_x, const LinearArgs a) {
@@ -739,11 +764,23 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       int st = 0;
       uint32_t ph = 0, acc_it = 0;
       for (int i = cid; alive && i < tiles; i += ncl, ++acc_it) {
-        const int buf = acc_it & 1;
+        int buf = acc_it & 1;
         if (!mbar_wait(&tempty_bar[buf], ((acc_it >> 1) & 1u) ^ 1u, abort_flag, a.err)) break;
         tc_fence_after();
-        const uint32_t d = tmem_base + buf * 256;
+        uint32_t d = tmem_base + buf * 256, acc = 0;
         for (int kb = kb0; kb < kb1; ++kb) {
+          if (WIDE && kb > kb0 && (kb - kb0) % kChain == 0) {  // the next accumulator
+            if (elect_one()) umma_commit_pair(&tfull_bar[buf], pair_mask);
+            __syncwarp();
+            buf = ++acc_it & 1;
+            if (!mbar_wait(&tempty_bar[buf], ((acc_it >> 1) & 1u) ^ 1u, abort_flag, a.err)) {
+              alive = false;
+              break;
+            }
+            tc_fence_after();
+            d = tmem_base + buf * 256;
+            acc = 0;
+          }
           if (!mbar_wait(&full_bar[st], ph, abort_flag, a.err)) {
             alive = false;
             break;
@@ -754,14 +791,68 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll
             for (int kk = 0; kk < kBK / 16; ++kk)
               umma_f16_pair(d, da + 2 * kk, da + (128 * 128 >> 4) + 2 * kk, idesc,
-                            (kb > kb0 || kk > 0) ? 1u : 0u);
+                            kk > 0 ? 1u : acc);
             umma_commit_pair(&empty_bar[st], pair_mask);
           }
           __syncwarp();
+          acc = 1;
           if (++st == kPairStages) st = 0, ph ^= 1;
         }
         if (alive && elect_one()) umma_commit_pair(&tfull_bar[buf], pair_mask);
         __syncwarp();
+      }
+    }
+  } else if constexpr (WIDE) {
+    const int ew = warp & 3, ch = (warp - 2) >> 2;
+    float* st = staged + (warp - 2) * 32 * kPairPitch;
+    constexpr int MINE = GATED ? 2 : 5;  // chunks ch, ch + 2, ... of this warp
+    uint32_t acc_it = 0;
+    bool alive = true;
+    for (int i = cid; alive && i < tiles; i += ncl) {
+      const Tile tl = tile_of(i);
+      const int trow0 = tl.t0 + rank * 128 + ew * 32;
+      const int chunks = (min(out_cols, a.N - tl.n0) + 15) / 16;
+      float v[MINE][16], u[GATED ? MINE : 1][16];
+      for (int kb = 0; kb < KB; kb += kChain, ++acc_it) {
+        const int buf = acc_it & 1;
+        const bool ok = mbar_wait(&tfull_bar[buf], (acc_it >> 1) & 1u, abort_flag, a.err);
+        if (named_bar_any(1, 32 * kPairEpiWarps, !ok || *abort_flag)) {
+          alive = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t tb = tmem_base + (static_cast<uint32_t>(ew * 32) << 16) + buf * 256;
+#pragma unroll
+        for (int k = 0; k < MINE; ++k) {
+          const int j = ch + 2 * k;
+          if (j < chunks) {
+            uint32_t x[16], y[16];
+            tmem_ld16(tb + 16 * j, x);
+            if constexpr (GATED) tmem_ld16(tb + half + 16 * j, y);
+            tmem_ld_wait();
+            reg_fence16(x);
+            if constexpr (GATED) reg_fence16(y);
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              v[k][c] = (kb == 0 ? 0.f : v[k][c]) + __uint_as_float(x[c]);
+              if constexpr (GATED)
+                u[k][c] = (kb == 0 ? 0.f : u[k][c]) + __uint_as_float(y[c]);
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(cluster_addr(&tempty_bar[buf], leader));
+      }
+      if (!alive) break;
+#pragma unroll
+      for (int k = 0; k < MINE; ++k) {
+        const int j = ch + 2 * k;
+        if (j < chunks) {
+          uint32_t raw[16];
+          if (a.residual) chunk_residual<VEC>(a, trow0, tl.n0 + 16 * j, raw);
+          chunk_finish<ACT, VEC>(a, trow0, tl.n0 + 16 * j, st, v[k], u[GATED ? k : 0], raw);
+        }
       }
     }
   } else if constexpr (!SPLIT) {
@@ -962,16 +1053,19 @@ int launch_row_act(int act, const CUtensorMap& tw, const CUtensorMap& tx, const 
 template <int ACT, bool VEC>
 int launch_pair(const CUtensorMap& tw, const CUtensorMap& tx, const LinearArgs& a, int num_sms,
                 cudaStream_t stream) {
-  static std::atomic<unsigned long long> split_set{0}, whole_set{0};
+  static std::atomic<unsigned long long> split_set{0}, whole_set{0}, wide_set{0};
   const int tiles = a.tiles_n * a.tiles_t;
   if (a.splits > 1) {
-    const auto kernel = linear_pair_kernel<ACT, VEC, true>;
+    const auto kernel = linear_pair_kernel<ACT, VEC, true, false>;
     if (!ensure_smem_limit(reinterpret_cast<const void*>(kernel), kPairSmem, split_set)) return -1;
     return launch_cluster(kernel, 2 * a.splits, 2 * a.splits * tiles, kPairThreads, kPairSmem,
                           stream, tw, tx, a);
   }
-  const auto kernel = linear_pair_kernel<ACT, VEC, false>;
-  if (!ensure_smem_limit(reinterpret_cast<const void*>(kernel), kPairSmem, whole_set)) return -1;
+  const auto kernel = a.out_f32 ? linear_pair_kernel<ACT, VEC, false, true>
+                                : linear_pair_kernel<ACT, VEC, false, false>;
+  if (!ensure_smem_limit(reinterpret_cast<const void*>(kernel), kPairSmem,
+                         a.out_f32 ? wide_set : whole_set))
+    return -1;
   const int pairs = tiles < num_sms / 2 ? tiles : num_sms / 2;
   return launch_cluster(kernel, 2, 2 * pairs, kPairThreads, kPairSmem, stream, tw, tx, a);
 }
@@ -993,7 +1087,7 @@ int launch_pair_act(int act, const CUtensorMap& tw, const CUtensorMap& tx, const
 // tile's shared memory fit 76, 36, 23, 15 times on 152 SMs.  What a launch
 // costs before its first and after its last K step: row tiles about 6000
 // cycles and 1500 more when split, pair tiles 7000 and 4000 more.
-LinearPlan plan_linear(int T, int K, int N, bool gated, int num_sms) {
+LinearPlan plan_linear(int T, int K, int N, bool gated, bool out_f32, int num_sms) {
   LinearPlan best{};
   const int KB = (K + kBK - 1) / kBK;
   if (T <= 16) {
@@ -1029,6 +1123,9 @@ LinearPlan plan_linear(int T, int K, int N, bool gated, int num_sms) {
     const double stage = 16384 + 128.0 * bn;
     const int ring = bn == 64 ? 3 : 4, fit = bn == 128 ? num_sms : 2 * num_sms;
     for (int s = 1; s <= 8 && s <= KB; s *= 2) {
+      // 32-bit outputs: chains of about kChain steps in the tile's accumulators
+      const int pieces = bn == 32 ? 8 : 4;
+      if (out_f32 && KB > s * pieces * kChain && s < 8 && 2 * s <= KB) continue;
       const double units = static_cast<double>(tn) * tt * s;
       const double share = bn == 128 || units <= num_sms ? 1.0 : 2.0;  // CTAs of an SM
       const double step = fmax(fmax(stage * share / ingest, turn / ring), issue);
@@ -1037,11 +1134,12 @@ LinearPlan plan_linear(int T, int K, int N, bool gated, int num_sms) {
     }
   }
   if (T > 64) {
-    for (int bn = 64; bn <= 256; bn += 32) {
+    const int widest = out_f32 ? (gated ? 128 : 160) : 256;
+    for (int bn = 64; bn <= widest; bn += 32) {
       const int oc = gated ? bn / 2 : bn;
       const int tn = (N + oc - 1) / oc, tt = (T + 255) / 256;
       const double step = fmax(fmax((16384 + 64.0 * bn) / ingest, issue), 2.0 * bn);
-      for (int s = 1; s <= 4 && s <= KB; ++s) {
+      for (int s = 1; s <= (out_f32 ? 1 : 4) && s <= KB; ++s) {
         const int fit = s == 1 ? num_sms / 2 : num_sms * (s == 2 ? 36 : s == 3 ? 23 : 15) / 152;
         const double waves = ceil(static_cast<double>(tn) * tt / (fit > 0 ? fit : 1));
         const double run = waves * (((KB + s - 1) / s) * step + (s > 1 ? 4000 : 0));

@@ -213,7 +213,7 @@ struct LinearPlan {
   int tiles_n, tiles_t;
   int splits;     // K splits of a tile (CTAs, or pairs, of its cluster)
 };
-LinearPlan plan_linear(int T, int K, int N, bool gated, int num_sms);
+LinearPlan plan_linear(int T, int K, int N, bool gated, bool out_f32, int num_sms);
 int launch_linear(const void* x, const void* w, const float* bias, int act, const void* residual,
                   int residual_f32, int T, int K, int N, void* out, int out_f32,
                   const LinearPlan& plan, int* err, int num_sms, cudaStream_t stream,
