@@ -1,0 +1,112 @@
+"""The block around the MoE layer, as a model's step runs it on one GPU:
+
+  h, y      = add_rms_norm(attention output, h)        residual stream, layer input
+  logits    = linear(y, gate) in f32                   kept for the balance loss
+  ids, w    = router(y, gate)                          the layer's own routing
+  loss, ... = balance_loss(logits, ids)                load statistics, gradient
+  m         = layer(y)                                 routed experts
+  a         = linear(y, shared w13, swiglu)            shared expert, up
+  o         = linear(a, shared w2, residual = m)       and down, added to the routed output
+  h, y'     = add_rms_norm(o, h)                       in front of what follows
+
+    python examples/moe_block.py [--workload qwen3] [--T 64] [--steps 20]
+
+prints the loss, the busiest and idlest expert, and the time of a step as one
+CUDA graph.  Random weights of the workload's shapes; with a low-bit workload
+(v4lo) the norm writes the experts' e4m3 codes and scales beside the rows.
+"""
+from __future__ import annotations
+
+import argparse
+import os
+import sys
+
+import torch
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+if ROOT not in sys.path:
+    sys.path.insert(0, ROOT)
+
+from router_experts_gb300 import moe  # noqa: E402
+from router_experts_gb300 import workloads as W  # noqa: E402
+
+EPS = 1e-6
+
+
+def make_params(w: W.Workload, shared: int, seed: int = 0, device="cuda") -> dict:
+    """Weights of one block: the workload's gate and experts, a shared expert of
+    `shared` hidden columns and two norms."""
+    d = W.make_inputs(w, 1, seed=seed, device=device)
+    g = torch.Generator(device=device)
+    g.manual_seed(seed + 1)
+
+    def normal(*shape, std):
+        return (torch.randn(shape, generator=g, device=device) * std).to(torch.bfloat16)
+
+    p = {k: v for k, v in d.items() if k not in ("hidden", "hidden_scale")}
+    p["shared_w13"] = normal(2 * shared, w.H, std=w.H ** -0.5)
+    p["shared_w2"] = normal(w.H, shared, std=shared ** -0.5)
+    for name in ("norm_in", "norm_out"):
+        p[name] = 1 + normal(w.H, std=0.1).float()
+    return p
+
+
+def moe_block(w: W.Workload, p: dict, attn: torch.Tensor, h: torch.Tensor, coef: float = 1e-3,
+              grad: bool = True, ws: moe.Workspace | None = None) -> dict:
+    """One block step; attn and h [T, H] bf16."""
+    h, y, codes, scales = moe.add_rms_norm(attn, p["norm_in"], h, EPS, e4m3=w.lowbit)
+    gate = p["gate"] if p["gate"].dtype == torch.bfloat16 else p["gate"].to(torch.bfloat16)
+    logits = moe.linear(y, gate, out_dtype=torch.float32, ws=ws)
+    routing = dict(n_group=w.n_group, topk_group=w.topk_group, renormalize=w.renormalize,
+                   scaling=w.scaling, ws=ws)
+    if w.lowbit:
+        ids, _ = moe.router(codes, p["gate"], p.get("bias"), w.k, w.scoring, hidden_scale=scales,
+                            **routing)
+        m = moe.layer(codes, p["gate"], p.get("bias"), p["w13"], p["w2"], w.k, w.scoring,
+                      hidden_scale=scales, w13_scale=p["w13_scale"], w2_scale=p["w2_scale"],
+                      **routing)
+    else:
+        ids, _ = moe.router(y, p["gate"], p.get("bias"), w.k, w.scoring, **routing)
+        m = moe.layer(y, p["gate"], p.get("bias"), p["w13"], p["w2"], w.k, w.scoring, **routing)
+    loss, counts, _, dlogits = moe.balance_loss(logits, ids, coef, w.scoring, grad=grad, ws=ws)
+    a = moe.linear(y, p["shared_w13"], activation="swiglu", ws=ws)
+    o = moe.linear(a, p["shared_w2"], residual=m, ws=ws)
+    h2, y2, _, _ = moe.add_rms_norm(o, p["norm_out"], h, EPS)
+    return {"h": h2, "y": y2, "loss": loss, "counts": counts, "dlogits": dlogits, "ids": ids,
+            "layer_in": y, "routed": m, "block": o, "h_in": h, "logits": logits}
+
+
+def main():
+    ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
+    ap.add_argument("--workload", default="qwen3", choices=["toy", "qwen3", "dsv3", "v4lo"])
+    ap.add_argument("--T", type=int, default=64)
+    ap.add_argument("--shared", type=int, default=0, help="shared expert's columns (default: F)")
+    ap.add_argument("--steps", type=int, default=20)
+    args = ap.parse_args()
+    w = W.WORKLOADS[args.workload]
+    p = make_params(w, args.shared or w.F)
+    attn, h = (torch.randn((args.T, w.H), device="cuda").to(torch.bfloat16) for _ in range(2))
+    ws = moe.Workspace("cuda")
+    ws.get(moe.layer_workspace_bytes(args.T, w.H, w.F, w.E, w.k,
+                                     act_dt=moe.DT_E4M3 if w.lowbit else moe.DT_BF16))
+    r = moe_block(w, p, attn, h, ws=ws)
+    torch.cuda.synchronize()
+    c = r["counts"][0]
+    print(f"{w.name} T={args.T}: balance loss {float(r['loss']):.6f}, assignments per expert "
+          f"{int(c.min())} to {int(c.max())} (mean {args.T * w.k / w.E:.1f})")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        moe_block(w, p, attn, h, ws=ws)
+    graph.replay()
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    start.record()
+    for _ in range(args.steps):
+        graph.replay()
+    end.record()
+    torch.cuda.synchronize()
+    print(f"one step as a graph: {start.elapsed_time(end) / args.steps * 1e3:.1f} us; "
+          f"device error word {moe.read_device_error(ws.buf)}")
+
+
+if __name__ == "__main__":
+    main()

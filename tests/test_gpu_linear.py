@@ -79,6 +79,17 @@ def test_shapes(T, K, N, act):
     check(moe.linear(x, w, b, act), x, w, b, act, None)
 
 
+@pytest.mark.parametrize("T", [1, 16, 40, 100, 300, 2000])
+@pytest.mark.parametrize("act", [None, "swiglu"])
+def test_long_sums_in_32_bits(T, act):
+    # a chain of 8192 terms on the tensor core is 9e-6 low; in pieces of 512 it
+    # is half a part in a million (twice that for the product of two such sums)
+    x, w, _, _ = make(T, 8192, 640, act, seed=T)
+    got = moe.linear(x, w, None, act, out_dtype=F32).double()
+    o, _ = reference(x, w, None, act, None)
+    assert float((got - o).norm() / o.norm()) <= (2e-6 if act else 1e-6)
+
+
 @pytest.mark.parametrize("T", [1, 2, 4, 5, 8, 15, 24, 48, 96, 200, 400, 640, 1100])
 @pytest.mark.parametrize("K,N", [(7168, 256), (2048, 768)])
 def test_tokens(T, K, N):
