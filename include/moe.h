@@ -1,7 +1,8 @@
 /*
  * moe.h -- C ABI of the GB300-native single-GPU Mixture-of-Experts layer
  * forward: router -> align -> expert GEMM1 + SwiGLU -> expert GEMM2 ->
- * weighted finalize.
+ * weighted finalize; and of the operators around it: residual addition +
+ * norm, dense product with epilogue, balance loss with its gradient.
  *
  * Pages the operations follow (cited per entry point below):
  *   [P1] "How an MoE Model Picks Its Experts During LLM Inference"
@@ -29,8 +30,9 @@
  *     it with moe_read_device_error.
  *   - Workspace: `ws` is caller-owned device memory of at least the size the
  *     matching *_workspace_bytes function returns, 256-byte aligned.  It must
- *     be zeroed once before its first use (moe_workspace_init); the library
- *     leaves it in a reusable state after every successful call.  Two calls
+ *     be zeroed once before its first use (moe_workspace_init), and again
+ *     after a MOE_DEVERR_WAIT_TIMEOUT; the library leaves it in a reusable
+ *     state after every successful call.  Two calls
  *     that overlap in time must not share a workspace.
  */
 #ifndef ROUTER_EXPERTS_GB300_MOE_H
@@ -63,14 +65,18 @@ typedef enum { MOE_DT_BF16 = 0, MOE_DT_F32 = 1, MOE_DT_E4M3 = 2, MOE_DT_E2M1 = 3
  * start; everything else in the header is the library's own):
  *   MOE_WS_ALIGN_BARRIER_OFFSET  int32[2]: arrival counter and generation of
  *                                the align kernel's grid barrier (0 at rest)
- *   MOE_WS_WAIT_LIMIT_OFFSET     int64: when > 0, the align kernel's grid
- *                                barrier gives up after this many SM clock
+ *   MOE_WS_BALANCE_BARRIER_OFFSET  int32: arrivals at the balance loss's grid
+ *                                barrier (0 at rest)
+ *   MOE_WS_WAIT_LIMIT_OFFSET     int64: when > 0, the grid barriers of the
+ *                                align kernel and of the balance loss give
+ *                                up after this many SM clock
  *                                cycles instead of about 2^32 (~2 s); a test
  *                                hook that makes the bounded-wait expiry
  *                                path cheap to exercise.  0 after
  *                                moe_workspace_init. */
 #define MOE_WS_ALIGN_BARRIER_OFFSET 5120
 #define MOE_WS_WAIT_LIMIT_OFFSET 5376
+#define MOE_WS_BALANCE_BARRIER_OFFSET 6400
 
 /* Bits of the device error word. */
 #define MOE_DEVERR_BAD_EXPERT_ID 1 /* an expert id outside [0,E) was skipped          */

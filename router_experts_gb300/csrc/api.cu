@@ -123,6 +123,7 @@ static const long long* wait_limit_word(void* ws) {
 }
 static_assert(kWsAlignBarrierOffset == MOE_WS_ALIGN_BARRIER_OFFSET, "header layout");
 static_assert(kWsWaitLimitOffset == MOE_WS_WAIT_LIMIT_OFFSET, "header layout");
+static_assert(kWsBalanceOffset == MOE_WS_BALANCE_BARRIER_OFFSET, "header layout");
 static_assert(kWsBalancePartOffset + 8 * kBalanceMaxSms <= kWsRouterTicketOffset, "header layout");
 
 // ---- checks -------------------------------------------------------------------
@@ -702,7 +703,7 @@ int moe_balance_loss(const void* logits, int logits_dt, const int32_t* topk_ids,
                           static_cast<long long>(B) * (E + 1) <= kAlignMaxCtas * kAlignMaxE
                               ? align_hist(ws)
                               : nullptr,
-                          err_word(ws),
+                          err_word(ws), wait_limit_word(ws),
                           sms < kBalanceMaxSms ? sms : kBalanceMaxSms,
                           static_cast<cudaStream_t>(stream)) != 0)
     return launch_fail("balance loss kernel");

@@ -40,10 +40,11 @@ struct BalanceArgs {
   float* loss;
   void* dlogits;
   float2* part;  // [grid] sums of the CTAs (pairs)
-  int* bars;     // two grid barriers {arrivals, generation}, then the ticket
+  int* bars;     // 0, 2: grid barriers' arrivals, 4: the ticket; zero between calls
   int* acc;      // [B][E + 1] counters, zero between calls: counts, then tokens;
                  // nullptr (too many): counts and tokens themselves, cleared first
   int* err;
+  const long long* wait_limit;  // workspace test hook: the barriers' limit in cycles, 0 = default
   float coef;
   int B, T, E, k;
   int chunk;     // tokens of a CTA
@@ -55,24 +56,19 @@ constexpr int kBalStarts = 1025;
 
 // A barrier over the grid in two halves: all threads of the CTA; what they
 // wrote before arrive is visible to whoever passes wait.  A grid of one
-// cluster uses the hardware's; a larger one (a cooperative launch) counts in
-// the workspace, its wait bounded as every wait.  gen (thread 0) is the
-// barrier's generation, read any time before arrive.
-MOE_DEV int bar_generation(bool cluster, const int* bar) {
-  return !cluster && threadIdx.x == 0 ? load_acquire_gpu(bar + 1) : 0;
-}
-MOE_DEV void bar_arrive(bool cluster, int* bar, int gen) {
+// cluster uses the hardware's; a larger one (a cooperative launch) counts
+// arrivals in the workspace, its wait bounded as every wait; the last CTA to
+// finish the kernel puts the count back to zero.
+MOE_DEV void bar_arrive(bool cluster, int* bar) {
   if (cluster) {
     cluster_arrive();
     return;
   }
   __syncthreads();
-  if (threadIdx.x == 0 && ticket_add_acq_rel(bar, 1) == static_cast<int>(gridDim.x) - 1) {
-    store_relaxed_gpu(bar, 0);
-    store_release_gpu(bar + 1, gen + 1);
-  }
+  if (threadIdx.x == 0)
+    asm volatile("red.add.release.gpu.global.s32 [%0], 1;" ::"l"(bar) : "memory");
 }
-MOE_DEV bool bar_wait(bool cluster, int* bar, int gen, int* err) {
+MOE_DEV bool bar_wait(bool cluster, int* bar, const long long* wait_limit, int* err) {
   if (cluster) {
     cluster_wait();
     return true;
@@ -81,8 +77,10 @@ MOE_DEV bool bar_wait(bool cluster, int* bar, int gen, int* err) {
   if (threadIdx.x == 0) {
     int good = 1;
     const long long t0 = clock64();
-    while (load_acquire_gpu(bar + 1) == gen) {
-      if (clock64() - t0 > kWaitLimitCycles) {
+    long long limit = 0;
+    while (load_acquire_gpu(bar) < static_cast<int>(gridDim.x)) {
+      if (limit == 0) limit = *wait_limit > 0 ? *wait_limit : kWaitLimitCycles;
+      if (clock64() - t0 > limit) {
         raise_error(err, kErrTimeout);
         good = 0;
         break;
@@ -309,18 +307,24 @@ __global__ void __launch_bounds__(kBalThreads, 1) balance_kernel(const BalanceAr
                                       static_cast<long long>(blockIdx.x) * a.chunk));
   const int t1 = static_cast<int>(min(static_cast<long long>(a.T),
                                       static_cast<long long>(t0) + a.chunk));
+  grid_dependency_launch();
+  grid_dependency_wait();
   const bool cl = a.cluster != 0;
-  const int gen = a.ids && G > 1 ? bar_generation(cl, a.bars) : 0;
-  if (a.ids) {  // this CTA's ids on their way while the starts are read
+  const int32_t* starts = a.starts;
+  int start0 = 0;
+  if (a.starts && a.B < kBalStarts) {
+    if (threadIdx.x <= a.B) start0 = __ldg(a.starts + threadIdx.x);
+    starts = starts_sm;
+  }
+  if (a.ids) {  // this CTA's ids on their way 
     const char* p = reinterpret_cast<const char*>(a.ids + static_cast<size_t>(t0) * a.k);
     const size_t bytes = static_cast<size_t>(t1 - t0) * a.k * 4;
     for (size_t i = threadIdx.x * size_t{128}; i < bytes; i += THREADS * size_t{128})
       asm volatile("prefetch.global.L2 [%0];" ::"l"(p + i));
   }
-  const int32_t* starts = a.starts;
   if (a.starts && a.B < kBalStarts) {
-    for (int i = threadIdx.x; i <= a.B; i += THREADS) starts_sm[i] = __ldg(a.starts + i);
-    starts = starts_sm;
+    if (threadIdx.x <= a.B) starts_sm[threadIdx.x] = start0;
+    for (int i = threadIdx.x + THREADS; i <= a.B; i += THREADS) starts_sm[i] = __ldg(a.starts + i);
   }
   if (threadIdx.x == 0) nseq = 0;
 
@@ -386,9 +390,8 @@ __global__ void __launch_bounds__(kBalThreads, 1) balance_kernel(const BalanceAr
       for (int i = first + threadIdx.x; i < min(cells, first + share_of); i += THREADS) cnt[i] = 0;
       for (int i = blockIdx.x * THREADS + threadIdx.x; i < a.B; i += G * THREADS) tok[i] = 0;
       if (G > 1) {
-        const int gen2 = bar_generation(cl, a.bars + 2);
-        bar_arrive(cl, a.bars + 2, gen2);
-        ok = bar_wait(cl, a.bars + 2, gen2, a.err);
+        bar_arrive(cl, a.bars + 2);
+        ok = bar_wait(cl, a.bars + 2, a.wait_limit, a.err);
       }
     }
     if (starts == starts_sm) __syncthreads();
@@ -502,9 +505,9 @@ __global__ void __launch_bounds__(kBalThreads, 1) balance_kernel(const BalanceAr
     // (only the first rows in front of the barrier: the others' traffic would
     // hold up its messages)
     if (G > 1) {
-      bar_arrive(cl, a.bars, gen);
+      bar_arrive(cl, a.bars);
       first_rows();
-      ok = bar_wait(cl, a.bars, gen, a.err) && ok;
+      ok = bar_wait(cl, a.bars, a.wait_limit, a.err) && ok;
       if (!ok) return;  // flagged; the outputs are not valid
     } else {
       first_rows();
@@ -519,6 +522,13 @@ __global__ void __launch_bounds__(kBalThreads, 1) balance_kernel(const BalanceAr
   // the counts of the CTA's first sequence to shared memory, once: every group
   // of every CTA reading them from the same few lines of L2 took 4 us
   const int bfirst = t0 < t1 ? sequence_of(starts, a.B, t0) : -1;
+  int holding = 0;  // of this thread's sequences, those that hold a counted token
+  if (a.starts) {
+    if (threadIdx.x < a.B)
+      holding = __ldcg(tok + static_cast<size_t>(threadIdx.x) * tpitch) > 0;
+    for (int i = threadIdx.x + THREADS; i < a.B; i += THREADS)
+      holding += __ldcg(tok + static_cast<size_t>(i) * tpitch) > 0;
+  }
   if (!local && bfirst >= 0) {
     for (int i = threadIdx.x; i < a.E; i += THREADS)
       hist[i] = __ldcg(cnt + static_cast<size_t>(bfirst) * pitch + i);
@@ -574,11 +584,8 @@ __global__ void __launch_bounds__(kBalThreads, 1) balance_kernel(const BalanceAr
   };
   // B': the sequences that hold a counted token
   if (a.starts) {
-    int mine = 0;
-    for (int i = threadIdx.x; i < a.B; i += THREADS)
-      mine += __ldcg(tok + static_cast<size_t>(i) * tpitch) > 0;
-    mine = __reduce_add_sync(0xffffffffu, mine);
-    if (lane == 0 && mine) atomicAdd(&nseq, mine);
+    holding = __reduce_add_sync(0xffffffffu, holding);
+    if (lane == 0 && holding) atomicAdd(&nseq, holding);
   }
   __syncthreads();
   Bp = a.starts ? nseq : 1;  // (without a counted token no share is taken)
@@ -730,7 +737,7 @@ __global__ void __launch_bounds__(kBalThreads, 1) balance_kernel(const BalanceAr
       } else {
         __stcg(a.part + blockIdx.x, make_float2(s.hi, s.lo));
         last = ticket_add_acq_rel(a.bars + 4, 1) == G - 1;
-        if (last) store_relaxed_gpu(a.bars + 4, 0);
+        if (last) a.bars[0] = a.bars[2] = a.bars[4] = 0;  // for the next call
       }
     }
     __syncwarp();
@@ -772,7 +779,7 @@ int launch_one(BalanceArgs a, int num_sms, cudaStream_t st) {
   a.chunk = static_cast<int>((static_cast<long long>(a.T) + grid - 1) / grid);
   a.cluster = cluster > 1;
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kBalThreads);
   cfg.dynamicSmemBytes = VEC ? kBalThreads * kBalDepth * SLOTS * (BF16 ? 2 : 4) : 0;
@@ -789,10 +796,15 @@ int launch_one(BalanceArgs a, int num_sms, cudaStream_t st) {
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.numAttrs = 1;
-  } else if (a.ids && grid > 1) {
+  }
+  if (a.ids && grid > 1 && cluster == 1) {
     attr[0].id = cudaLaunchAttributeCooperative;
     attr[0].val.cooperative = 1;
     cfg.numAttrs = 1;
+  } else {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+    ++cfg.numAttrs;
   }
   if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) return -1;
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
@@ -824,8 +836,8 @@ int launch_scoring(const BalanceArgs& a, int scoring, bool bf16, bool vec, int s
 int launch_balance_loss(const void* logits, bool bf16, const int32_t* ids, const uint8_t* mask,
                         const int32_t* starts, int B, int T, int E, int k, int scoring,
                         float coef, float* loss, int32_t* counts, int32_t* tokens, void* dlogits,
-                        bool vec, float2* part, int* bars, int* acc, int* err, int num_sms,
-                        cudaStream_t st) {
+                        bool vec, float2* part, int* bars, int* acc, int* err,
+                        const long long* wait_limit, int num_sms, cudaStream_t st) {
   if (T == 0) {
     const bool done = cudaMemsetAsync(counts, 0, static_cast<size_t>(B) * E * 4, st) == cudaSuccess &&
                       cudaMemsetAsync(tokens, 0, static_cast<size_t>(B) * 4, st) == cudaSuccess &&
@@ -845,6 +857,7 @@ int launch_balance_loss(const void* logits, bool bf16, const int32_t* ids, const
   a.bars = bars;
   a.acc = acc;
   a.err = err;
+  a.wait_limit = wait_limit;
   a.coef = coef;
   a.B = B;
   a.T = T;

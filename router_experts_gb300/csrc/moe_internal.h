@@ -21,7 +21,7 @@ constexpr size_t kWsAlignBarrierOffset = 5120;      // int32[2] grid barrier of 
 constexpr size_t kWsAlignTicketOffset = 5128;       // int32 align: CTAs done reading the counts
 constexpr size_t kWsWaitLimitOffset = 5376;         // int64 test hook: align barrier limit (cycles)
 constexpr size_t kWsDecodeCounterOffset = 6144;     // int32[3] persistent layer: routed, zeroed, done
-constexpr size_t kWsBalanceOffset = 6400;           // int32[5] balance loss: grid barriers, ticket
+constexpr size_t kWsBalanceOffset = 6400;           // int32[5] balance loss: barriers 0 and 2, ticket 4
 constexpr size_t kWsBalancePartOffset = 6528;       // float2[kBalanceMaxSms] CTAs' sums
 constexpr int kBalanceMaxSms = 200;
 constexpr size_t kWsRouterTicketOffset = 8192;      // int32[kRouterMaxTiles]
@@ -221,13 +221,13 @@ int launch_linear(const void* x, const void* w, const float* bias, int act, cons
 
 // ---- balance loss (balance.cu) --------------------------------------------------------
 // vec: E % 4 == 0 and logits / dlogits aligned to four elements.  part: one
-// pair per SM; bars: int32[5], zero before the first call, self-resetting; acc:
+// pair per SM; bars: int32[5], zero between calls (see balance.cu); acc:
 // int32[B * (E + 1)], zero between calls, or nullptr.
 int launch_balance_loss(const void* logits, bool bf16, const int32_t* ids, const uint8_t* mask,
                         const int32_t* starts, int B, int T, int E, int k, int scoring,
                         float coef, float* loss, int32_t* counts, int32_t* tokens, void* dlogits,
-                        bool vec, float2* part, int* bars, int* acc, int* err, int num_sms,
-                        cudaStream_t st);
+                        bool vec, float2* part, int* bars, int* acc, int* err,
+                        const long long* wait_limit, int num_sms, cudaStream_t st);
 int launch_balance_loss_backward(const float* dloss, const void* logits, bool bf16,
                                  const int32_t* counts, const int32_t* tokens,
                                  const uint8_t* mask, const int32_t* starts, int B, int T, int E,

@@ -26,6 +26,7 @@ ACTIVATIONS = {None: 0, "silu": 1, "gelu": 2, "swiglu": 3}
 DEVERR_BAD_EXPERT_ID, DEVERR_WAIT_TIMEOUT, DEVERR_BAD_TABLE = 1, 2, 4
 # workspace header words a test may set (include/moe.h)
 WS_ALIGN_BARRIER_OFFSET, WS_WAIT_LIMIT_OFFSET = 5120, 5376
+WS_BALANCE_BARRIER_OFFSET = 6400
 
 _lock = threading.Lock()
 _lib = None

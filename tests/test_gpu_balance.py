@@ -132,6 +132,25 @@ def test_many_short_sequences():
     check(logits, ids, "softmax", mask, torch.arange(0, 3001, 3, dtype=torch.int32, device="cuda"))
 
 
+def test_more_sequences_than_counters():
+    # B (E + 1) past the workspace's table, B past the starts in shared memory
+    T, E = 9000, 512
+    logits, ids, mask = make(T, E, 2, seed=9)
+    check(logits, ids, "sigmoid", mask, torch.arange(0, T + 1, 60, dtype=torch.int32, device="cuda"))
+    logits, ids, mask = make(T, 16, 2, seed=10)
+    check(logits, ids, "softmax", mask, torch.arange(0, T + 1, 5, dtype=torch.int32, device="cuda"))
+    check(logits[:40], ids[:40], "softmax", mask[:40],
+          torch.arange(0, 41, 1, dtype=torch.int32, device="cuda"))
+
+
+@pytest.mark.parametrize("T", [97, 500, 513, 1500])
+def test_one_cta_cluster_and_grid(T):
+    # one CTA up to 96 tokens of this width, one cluster up to 512, then the grid
+    logits, ids, mask = make(T, 256, 8, seed=T)
+    check(logits, ids, "sigmoid")
+    check(logits, ids, "softmax", mask, starts_of(0, T // 3, T // 3 + 2, T))
+
+
 @pytest.mark.parametrize("scoring", SCORINGS)
 def test_nothing_counted(scoring):
     logits, ids, mask = make(50, 16, 2, seed=1)
@@ -224,6 +243,30 @@ def test_same_bits_every_time():
     for _ in range(3):
         again = moe.balance_loss(logits, ids, COEF, "sigmoid", token_mask=mask, grad=True)
         assert all(torch.equal(a, b) for a, b in zip(first, again))
+
+
+def test_barrier_wait_expires_and_reports():
+    # arrivals preset far below zero never reach the grid's size: the wait runs
+    # out (a millisecond by the test hook) and is reported; the tokens' outputs
+    # stay as they were, and a zeroed workspace works again
+    logits, ids, _ = make(2000, 64, 4, seed=7)
+    ws = moe.Workspace("cuda")
+    moe.balance_loss(logits, ids, COEF, ws=ws)
+    head = ws.buf[:8192]
+    head[moe.WS_BALANCE_BARRIER_OFFSET:][:4].view(torch.int32).fill_(-2 ** 30)
+    head[moe.WS_WAIT_LIMIT_OFFSET:][:8].view(torch.int64).fill_(2 ** 21)
+    out = (torch.full((1,), 7.0, device="cuda"),
+           torch.empty((1, 64), dtype=torch.int32, device="cuda"),
+           torch.empty(1, dtype=torch.int32, device="cuda"), torch.full_like(logits, 7.0))
+    moe.balance_loss(logits, ids, COEF, grad=True, ws=ws, out=out)
+    assert moe.read_device_error(ws.buf) == moe.DEVERR_WAIT_TIMEOUT
+    assert float(out[0]) == 7 and (out[3] == 7).all()
+    ws.buf.zero_()
+    loss, counts, tokens, dl, tol = reference(logits, ids, "softmax")
+    got = moe.balance_loss(logits, ids, COEF, grad=True, ws=ws)
+    assert torch.equal(got[1], counts)
+    assert ((got[3].double() - dl).abs() <= tol + dl.abs() * 2.0 ** -24 + 1e-38).all()
+    assert moe.read_device_error(ws.buf) == 0
 
 
 def test_no_tokens():

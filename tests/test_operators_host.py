@@ -117,6 +117,16 @@ def test_binding_refuses_host_tensors_and_wrong_shapes(lib):
         moe.linear(x[0], x)
 
 
+def test_balance_header_word_matches_the_binding():
+    import os
+    import re
+    from router_experts_gb300 import moe
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    src = open(os.path.join(root, "include", "moe.h")).read()
+    defs = dict(re.findall(r"#define\s+(MOE_WS_\w+)\s+(\d+)", src))
+    assert int(defs["MOE_WS_BALANCE_BARRIER_OFFSET"]) == moe.WS_BALANCE_BARRIER_OFFSET
+
+
 @pytest.mark.gpu
 def test_binding_refuses_what_the_kernels_cannot_hold():
     from router_experts_gb300 import moe
