@@ -242,14 +242,18 @@ MOE_DEV int expert_of(int r, int i) {
 // weighs nothing.
 template <int SLOTS, bool BF16>
 MOE_DEV void load_row(const void* logits, size_t row, int lane, int E, float (&l)[SLOTS]) {
+  // (every lane loads, the last expert past E: a load in a branch of its own
+  // would be waited for there)
+  uint32_t raw[SLOTS];
 #pragma unroll
   for (int i = 0; i < SLOTS; ++i) {
-    const int e = i * 32 + lane;
-    l[i] = -INFINITY;
-    if (e < E)
-      l[i] = BF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(logits)[row + e])
-                  : static_cast<const float*>(logits)[row + e];
+    const size_t at = row + min(i * 32 + lane, E - 1);
+    raw[i] = BF16 ? static_cast<const uint16_t*>(logits)[at]
+                  : static_cast<const uint32_t*>(logits)[at];
   }
+#pragma unroll
+  for (int i = 0; i < SLOTS; ++i)
+    l[i] = i * 32 + lane < E ? __uint_as_float(BF16 ? raw[i] << 16 : raw[i]) : -INFINITY;
 }
 
 template <bool VEC, int LPT, int SLOTS, bool BF16>

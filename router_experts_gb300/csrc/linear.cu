@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(32 * kTokMaxWarps, 2)
 // row, so the 32 lanes of a warp write 32 neighbouring outputs of one token at
 // any alignment of N.
 //   warp 0     TMA producer      warp 1    TMEM allocation, MMA issue
-//   warps 2-5  epilogue
+//   warps 2-9  epilogue, two per TMEM lane quarter
 // ---------------------------------------------------------------------------
 template <int BN>
 struct RowCfg {
@@ -257,13 +257,14 @@ struct RowCfg {
   static constexpr int STAGES = BN == 64 ? 3 : 4;
   static constexpr int PIECES = BN == 32 ? 8 : 4;  // accumulators of a chain's pieces
   static constexpr int TMEM_COLS = PIECES * BN;    // two CTAs share an SM's 512 (BN <= 64)
-  static constexpr int THREADS = 192;
+  static constexpr int EPI_WARPS = 8;
+  static constexpr int THREADS = 64 + 32 * EPI_WARPS;
   static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + RECV_BYTES + 1024 + 256;
   static_assert(SMEM_BYTES <= (BN == 128 ? 232448 : 232448 / 2 - 1024), "shared memory budget");
 };
 
 template <int ACT, int BN>
-__global__ void __launch_bounds__(RowCfg<BN>::THREADS)
+__global__ void __launch_bounds__(RowCfg<BN>::THREADS, BN == 128 ? 1 : 2)
     linear_row_kernel(const __grid_constant__ CUtensorMap tm_w,
                       const __grid_constant__ CUtensorMap tm_x, const LinearArgs a) {
   using C = RowCfg<BN>;
@@ -287,8 +288,8 @@ __global__ void __launch_bounds__(RowCfg<BN>::THREADS)
   const int KB = (a.K + kBK - 1) / kBK;
   int kb0, kb1;
   split_range(KB, S, s, &kb0, &kb1);
-  // the chain in pieces of whole steps, each with its own accumulator
-  const int piece = (kb1 - kb0 + C::PIECES - 1) / C::PIECES;
+  // a 32-bit output's chain in pieces of whole steps, each with its own accumulator
+  const int piece = a.out_f32 ? (kb1 - kb0 + C::PIECES - 1) / C::PIECES : kb1 - kb0;
   const int pieces = (kb1 - kb0 + piece - 1) / piece;
 
   grid_dependency_launch();
@@ -373,40 +374,41 @@ __global__ void __launch_bounds__(RowCfg<BN>::THREADS)
   const int cols = min(BN, a.T - t0);
   const int mine = min(P, cols - s * P);  // token columns that this CTA owns
   const int ew = warp & 3;                // a warp reads the TMEM lane quarter warp % 4
+  const int ch = (warp - 2) >> 2;         // and every other chunk of 16 token columns
   const int row = ew * 32 + lane;
-  // thread -> output column and first token of the epilogue: gated tiles have
-  // 64 columns, and their two halves of the threads take tokens in turn
+  // thread -> output column and first tokens of the epilogue, U tokens a read:
+  // the two halves of the threads (gated, with 64 columns: four quarters) take
+  // the reads in turn
   const int r = GATED ? (row & 63) : row;
   const int n = n0 + r;
-  constexpr int U = 4;                       // tokens of a 16-byte read
-  constexpr int STEP = GATED ? 2 * U : U;
-  const int first = GATED ? (row >> 6) * U : 0;
-  constexpr int KEEP = 8;                    // reads whose residual is fetched ahead
-  float res[KEEP][U];
-  auto load_residual = [&](int p0, float (&v)[U]) {
-    const size_t at = static_cast<size_t>(t0 + s * P + p0) * a.N + n;
-    if (a.residual_f32) {
+  constexpr int U = 4;
+  constexpr int STEP = (GATED ? 4 : 2) * U;
+  const int first = (GATED ? 2 * ch + (row >> 6) : ch) * U;
+  constexpr int KEEP = 4;  // reads whose residual is fetched ahead
+  uint32_t res[KEEP][U];
+  // (every thread loads, the last token or column past the end: a load in a
+  // branch of its own would be waited for there)
+  auto load_residual = [&](int p0, uint32_t (&v)[U]) {
+    const int c = min(n, a.N - 1);
 #pragma unroll
-      for (int i = 0; i < U; ++i)
-        v[i] = p0 + i < mine ? static_cast<const float*>(a.residual)[at + static_cast<size_t>(i) * a.N] : 0.f;
-    } else {
-#pragma unroll
-      for (int i = 0; i < U; ++i)
-        v[i] = p0 + i < mine ? __bfloat162float(static_cast<const __nv_bfloat16*>(
-                                   a.residual)[at + static_cast<size_t>(i) * a.N])
-                             : 0.f;
+    for (int i = 0; i < U; ++i) {
+      const size_t at = static_cast<size_t>(min(t0 + s * P + p0 + i, a.T - 1)) * a.N + c;
+      v[i] = a.residual_f32 ? static_cast<const uint32_t*>(a.residual)[at]
+                            : static_cast<const uint16_t*>(a.residual)[at];
     }
   };
+  const int res_shift = a.residual_f32 ? 0 : 16;
   bool ok = true;
   if (warp >= 2) {
     grid_dependency_wait();
 #pragma unroll
     for (int k = 0; k < KEEP; ++k)
 #pragma unroll
-      for (int i = 0; i < U; ++i) res[k][i] = 0.f;
-    if (a.residual && n < a.N) {
+      for (int i = 0; i < U; ++i) res[k][i] = 0;  // adds a zero where there is none
+    if (a.residual && mine > 0) {
 #pragma unroll
-      for (int k = 0; k < KEEP; ++k) load_residual(first + k * STEP, res[k]);
+      for (int k = 0; k < KEEP; ++k)
+        if (first + k * STEP < mine) load_residual(first + k * STEP, res[k]);
     }
     ok = mbar_wait(done_bar, 0, abort_flag, a.err);
     tc_fence_after();
@@ -416,21 +418,25 @@ __global__ void __launch_bounds__(RowCfg<BN>::THREADS)
   if (warp >= 2) {
     if (ok) {
       const float* to = recv + s * P * 128 + row * 4;
+      const uint32_t tq = tmem_base + (static_cast<uint32_t>(ew * 32) << 16);
 #pragma unroll 1
-      for (int c0 = 0; c0 < cols; c0 += 16) {
-        const uint32_t tb = tmem_base + (static_cast<uint32_t>(ew * 32) << 16) + c0;
-        uint32_t v[16];
-        tmem_ld16(tb, v);
+      for (int c0 = 16 * ch; c0 < cols; c0 += 32) {
+        uint32_t v[16], w[16];
+        tmem_ld16(tq + c0, v);
+        if (pieces > 1) tmem_ld16(tq + BN + c0, w);
         tmem_ld_wait();
         reg_fence16(v);
-        for (int p = 1; p < pieces; ++p) {
-          uint32_t w[16];
-          tmem_ld16(tb + p * BN, w);
-          tmem_ld_wait();
+        for (int p = 1; p < pieces; ++p) {  // the next piece's sums on their way
+          uint32_t z[16];
           reg_fence16(w);
+          if (p + 1 < pieces) tmem_ld16(tq + (p + 1) * BN + c0, z);
 #pragma unroll
           for (int c = 0; c < 16; ++c)
             v[c] = __float_as_uint(__uint_as_float(v[c]) + __uint_as_float(w[c]));
+          tmem_ld_wait();
+          reg_fence16(z);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) w[c] = z[c];
         }
 #pragma unroll
         for (int c = 0; c < 16; c += U) {
@@ -452,7 +458,7 @@ __global__ void __launch_bounds__(RowCfg<BN>::THREADS)
       bg = __ldg(a.bias + n);
       if constexpr (GATED) bu = __ldg(a.bias + a.N + n);
     }
-    auto finish = [&](int p0, const float (&rs)[U]) {
+    auto finish = [&](int p0, const uint32_t (&rs)[U]) {
       float v[U], u[U];
 #pragma unroll
       for (int i = 0; i < U; ++i) v[i] = u[i] = 0.f;
@@ -466,7 +472,8 @@ __global__ void __launch_bounds__(RowCfg<BN>::THREADS)
         }
       }
 #pragma unroll
-      for (int i = 0; i < U; ++i) v[i] = activate(ACT, v[i] + bg, u[i] + bu) + rs[i];
+      for (int i = 0; i < U; ++i)
+        v[i] = activate(ACT, v[i] + bg, u[i] + bu) + __uint_as_float(rs[i] << res_shift);
       const size_t at = static_cast<size_t>(t0 + s * P + p0) * a.N + n;
       if (a.out_f32) {
 #pragma unroll
@@ -486,7 +493,8 @@ __global__ void __launch_bounds__(RowCfg<BN>::THREADS)
     for (int p0 = first + KEEP * STEP; p0 < mine; p0 += KEEP * STEP) {
       if (a.residual) {
 #pragma unroll
-        for (int k = 0; k < KEEP; ++k) load_residual(p0 + k * STEP, res[k]);
+        for (int k = 0; k < KEEP; ++k)
+          if (p0 + k * STEP < mine) load_residual(p0 + k * STEP, res[k]);
       }
 #pragma unroll
       for (int k = 0; k < KEEP; ++k)
@@ -525,6 +533,19 @@ constexpr int kPairStagedBytes = kPairEpiWarps * 32 * kPairPitch * 4;
 constexpr int kPairSmem = kPairStages * kPairStageBytes + 1024 + 512 + kPairStagedBytes;
 static_assert(kPairSmem <= 232448, "shared memory budget");
 
+// The residual's lines of this lane's token for columns [n, n + cols) into L2
+// while the MMAs run (read by chunks from HBM, it held the epilogue up by a
+// memory latency a chunk).  part: two warps share the lines.
+MOE_DEV void prefetch_residual(const LinearArgs& a, int t, int n, int cols, int part) {
+  if (!a.residual || t >= a.T || n >= a.N || cols <= 0) return;
+  const int size = a.residual_f32 ? 4 : 2;
+  const char* first = static_cast<const char*>(a.residual) + (static_cast<size_t>(t) * a.N + n) * size;
+  const char* last = first + static_cast<size_t>(min(cols, a.N - n)) * size - 1;
+  for (const char* p = first + 128 * part; p <= last; p += 256)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+  if (part == 0) asm volatile("prefetch.global.L2 [%0];" ::"l"(last));
+}
+
 // A chunk is 16 output columns n .. n + 15 (n < N) of the 32 tokens trow0 ..
 // trow0 + 31.  VEC (N % 16 == 0, 32-byte bases): a lane has one token and moves
 // its 16 values as vectors.  Otherwise, rows of N elements at any alignment:
@@ -550,22 +571,19 @@ MOE_DEV void chunk_residual(const LinearArgs& a, int trow0, int n, uint32_t (&ra
       }
     }
   } else {
-    const int c = lane & 15, tq = trow0 + (lane >> 4);
-    const size_t p0 = static_cast<size_t>(tq) * a.N + n + c;
-    const int rows = n + c < a.N ? a.T - tq : 0;
+    // (every lane loads, the last row or column past the end: a load in a
+    // branch of its own would be waited for there)
+    const int c = min(n + (lane & 15), a.N - 1), tq = trow0 + (lane >> 4);
     if (a.residual_f32) {
 #pragma unroll
       for (int j = 0; j < 16; ++j)
-        if (2 * j < rows)
-          raw[j] = __float_as_uint(
-              static_cast<const float*>(a.residual)[p0 + static_cast<size_t>(2 * j) * a.N]);
+        raw[j] = static_cast<const uint32_t*>(
+            a.residual)[static_cast<size_t>(min(tq + 2 * j, a.T - 1)) * a.N + c];
     } else {
 #pragma unroll
       for (int j = 0; j < 16; ++j)
-        if (2 * j < rows)
-          raw[j] = static_cast<uint32_t>(static_cast<const uint16_t*>(
-                       a.residual)[p0 + static_cast<size_t>(2 * j) * a.N])
-                   << 16;
+        raw[j] = static_cast<const uint16_t*>(
+            a.residual)[static_cast<size_t>(min(tq + 2 * j, a.T - 1)) * a.N + c];
     }
   }
 }
@@ -625,8 +643,9 @@ MOE_DEV void chunk_finish(const LinearArgs& a, int trow0, int n, float* staged, 
 #pragma unroll
     for (int j = 0; j < 16; ++j) o[j] = from[2 * j * kPairPitch];
     if (a.residual) {
+      const int shift = a.residual_f32 ? 0 : 16;
 #pragma unroll
-      for (int j = 0; j < 16; ++j) o[j] += __uint_as_float(raw[j]);
+      for (int j = 0; j < 16; ++j) o[j] += __uint_as_float(raw[j] << shift);
     }
     if (a.out_f32) {
 #pragma unroll
@@ -813,6 +832,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       const int trow0 = tl.t0 + rank * 128 + ew * 32;
       const int chunks = (min(out_cols, a.N - tl.n0) + 15) / 16;
       float v[MINE][16], u[GATED ? MINE : 1][16];
+      prefetch_residual(a, trow0 + lane, tl.n0, out_cols, ch);
       for (int kb = 0; kb < KB; kb += kChain, ++acc_it) {
         const int buf = acc_it & 1;
         const bool ok = mbar_wait(&tfull_bar[buf], (acc_it >> 1) & 1u, abort_flag, a.err);
@@ -866,6 +886,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       const int trow0 = tl.t0 + rank * 128 + ew * 32;  // token of lane 0
       const int chunks = (min(out_cols, a.N - tl.n0) + 15) / 16;
       uint32_t raw[16];
+      prefetch_residual(a, trow0 + lane, tl.n0, out_cols, ch);
       if (a.residual && ch < chunks) chunk_residual<VEC>(a, trow0, tl.n0 + 16 * ch, raw);
       const bool ok = mbar_wait(&tfull_bar[buf], (acc_it >> 1) & 1u, abort_flag, a.err);
       if (named_bar_any(1, 32 * kPairEpiWarps, !ok || *abort_flag)) break;
@@ -907,6 +928,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     uint32_t raw[16];
     bool ok = true;
     if (warp >= 2) {
+      prefetch_residual(a, trow0 + lane, tl.n0 + 16 * pr * own, 16 * own, ch);
       if (a.residual && pr * own + ch < end)
         chunk_residual<VEC>(a, trow0, tl.n0 + 16 * (pr * own + ch), raw);
       ok = mbar_wait(&tfull_bar[0], 0, abort_flag, a.err);
@@ -915,28 +937,33 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     __syncwarp();
     cluster_sync_all();  // every ring of the cluster is done with
     if (warp >= 2 && ok) {
-#pragma unroll 1
-      for (int j = ch; j < chunks; j += 2) {
+      uint32_t x[2][16], y[2][16];
+      auto load = [&](int j, int b) {
+        tmem_ld16(tb + 16 * j, x[b]);
+        if constexpr (GATED) tmem_ld16(tb + half + 16 * j, y[b]);
+      };
+      if (ch < chunks) load(ch, 0);
+#pragma unroll 2
+      for (int j = ch, b = 0; j < chunks; j += 2, b ^= 1) {
+        tmem_ld_wait();
+        reg_fence16(x[b]);
+        if constexpr (GATED) reg_fence16(y[b]);
+        if (j + 2 < chunks) load(j + 2, b ^ 1);
         const int q = j / own;
         if (q == pr) continue;
         const int from = pr < q ? pr : pr - 1;  // this split's slot at owner q
         const uint32_t dst =
             cluster_addr(recv + ((from * own + j - q * own) * W * 128 + row * 4), 2 * q + rank);
-        uint32_t x[16], y[16];
-        tmem_ld16(tb + 16 * j, x);
-        if constexpr (GATED) tmem_ld16(tb + half + 16 * j, y);
-        tmem_ld_wait();
-        reg_fence16(x);
 #pragma unroll
         for (int c = 0; c < 16; c += 4)
-          st_cluster_v4(dst + 512 * c, x[c], x[c + 1], x[c + 2], x[c + 3]);
+          st_cluster_v4(dst + 512 * c, x[b][c], x[b][c + 1], x[b][c + 2], x[b][c + 3]);
         if constexpr (GATED) {
-          reg_fence16(y);
 #pragma unroll
           for (int c = 0; c < 16; c += 4)
-            st_cluster_v4(dst + 512 * (16 + c), y[c], y[c + 1], y[c + 2], y[c + 3]);
+            st_cluster_v4(dst + 512 * (16 + c), y[b][c], y[b][c + 1], y[b][c + 2], y[b][c + 3]);
         }
       }
+      tmem_ld_wait();
     }
     __syncwarp();
     cluster_sync_all();
