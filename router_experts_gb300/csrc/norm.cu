@@ -340,55 +340,90 @@ __global__ void __launch_bounds__(IT == 1 ? 256 : 1024) norm_window_kernel(const
   grid_dependency_launch();
   grid_dependency_wait();
   const size_t total = static_cast<size_t>(a.T) * a.H;
-  // sums of the IT vectors of row t; elements [lo, hi) of a vector are the row's
+  // the IT vectors of a row as they lie in memory: they are turned into sums
+  // only when the row's turn comes, so that the next row stays in flight
+  constexpr int XW = XF32 ? 2 : 1, RW = RES == 0 ? 1 : RES;
+  struct Raw {
+    uint4 x[IT][XW], r[IT][RW];
+  };
+  // elements [lo, hi) of vector v are the row's
   auto bounds = [&](size_t row, int v, int* lo, int* hi) {
     const int j = 8 * v - static_cast<int>(row & 7);
     *lo = max(0, -j);
     *hi = min(8, a.H - j);
   };
-  auto load = [&](long long t, float (&s)[IT][8]) {
+  auto load = [&](long long t, Raw& raw) {
+    const size_t row = static_cast<size_t>(t) * a.H;
+#pragma unroll
+    for (int k = 0; k < IT; ++k) {
+      const int v = tid + k * blockDim.x;
+      // whole vectors, also where a neighbouring row owns a part; what lies past
+      // the row or reaches past the tensor takes the last whole vector instead
+      size_t at = (row & ~size_t{7}) + 8 * static_cast<size_t>(v);
+      if (at + 8 > total) at = (total & ~size_t{7}) - 8;
+      const uint4* x = reinterpret_cast<const uint4*>(static_cast<const char*>(a.x) +
+                                                      at * (XF32 ? 4 : 2));
+#pragma unroll
+      for (int i = 0; i < XW; ++i) raw.x[k][i] = x[i];
+      if constexpr (RES != 0) {
+        const uint4* r = reinterpret_cast<const uint4*>(static_cast<const char*>(a.res) +
+                                                        at * (RES == 2 ? 4 : 2));
+#pragma unroll
+        for (int i = 0; i < RW; ++i) raw.r[k][i] = r[i];
+      }
+    }
+  };
+  auto values = [&](const uint4* w, bool f32, float (&v)[8]) {
+    const uint32_t u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+    if (f32) {
+      const uint32_t u2[4] = {w[1].x, w[1].y, w[1].z, w[1].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] = __uint_as_float(u[i]);
+        v[4 + i] = __uint_as_float(u2[i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(u[i] << 16);
+        v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+      }
+    }
+  };
+  auto sums = [&](long long t, const Raw& raw, float (&s)[IT][8]) {
     const size_t row = static_cast<size_t>(t) * a.H;
 #pragma unroll
     for (int k = 0; k < IT; ++k) {
       const int v = tid + k * blockDim.x;
       int lo, hi;
       bounds(row, v, &lo, &hi);
-      const size_t at = (row & ~size_t{7}) + 8 * static_cast<size_t>(v);
-      // whole vectors also where a neighbouring row owns a part (a branch of
-      // its own for the ends would wait for memory twice); only what reaches
-      // past the tensor goes by elements
-      if (at + 8 <= total) {
-        if (hi > lo) {
-          if constexpr (XF32) load_f32<8>(static_cast<const float*>(a.x) + at, s[k]);
-          else load_bf16<8>(static_cast<const __nv_bfloat16*>(a.x) + at, s[k]);
-          if constexpr (RES != 0) {
-            float q[8];
-            if constexpr (RES == 2) load_f32<8>(static_cast<const float*>(a.res) + at, q);
-            else load_bf16<8>(static_cast<const __nv_bfloat16*>(a.res) + at, q);
+      values(raw.x[k], XF32, s[k]);
+      if constexpr (RES != 0) {
+        float q[8];
+        values(raw.r[k], RES == 2, q);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s[k][i] += q[i];
-          }
-        }
-      } else {
+        for (int i = 0; i < 8; ++i) s[k][i] += q[i];
+      }
+      const size_t at = (row & ~size_t{7}) + 8 * static_cast<size_t>(v);
+      if (at + 8 > total && hi > lo) {  // the tensor's last elements, one by one
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          float v1 = 0.f;
           if (i >= lo && i < hi) {
-            v1 = XF32 ? static_cast<const float*>(a.x)[at + i]
-                      : __bfloat162float(static_cast<const __nv_bfloat16*>(a.x)[at + i]);
+            float v1 = XF32 ? static_cast<const float*>(a.x)[at + i]
+                            : __bfloat162float(static_cast<const __nv_bfloat16*>(a.x)[at + i]);
             if constexpr (RES == 1)
               v1 += __bfloat162float(static_cast<const __nv_bfloat16*>(a.res)[at + i]);
             if constexpr (RES == 2) v1 += static_cast<const float*>(a.res)[at + i];
+            s[k][i] = v1;
           }
-          s[k][i] = v1;
         }
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) s[k][i] = i >= lo && i < hi ? s[k][i] : 0.f;
     }
   };
-  float s[IT][8];
-  load(blockIdx.x, s);
+  Raw raw;
+  load(blockIdx.x, raw);
   {  // the weights, four loads of a thread at a time
     for (int i0 = tid; i0 < a.H; i0 += 4 * blockDim.x) {
       float w[4][1];
@@ -405,6 +440,8 @@ __global__ void __launch_bounds__(IT == 1 ? 256 : 1024) norm_window_kernel(const
   __syncthreads();
   int buf = 0;
   for (long long t = blockIdx.x; t < a.T; t += gridDim.x) {
+    float s[IT][8];
+    sums(t, raw, s);
     float sum = 0.f;
 #pragma unroll
     for (int k = 0; k < IT; ++k)
@@ -414,8 +451,7 @@ __global__ void __launch_bounds__(IT == 1 ? 256 : 1024) norm_window_kernel(const
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) part[buf][warp] = sum;
     // the next row is in flight while this one is finished
-    float next[IT][8];
-    if (t + gridDim.x < a.T) load(t + gridDim.x, next);
+    if (t + gridDim.x < a.T) load(t + gridDim.x, raw);
     __syncthreads();
     sum = lane < warps ? part[buf][lane] : 0.f;
 #pragma unroll
@@ -453,10 +489,6 @@ __global__ void __launch_bounds__(IT == 1 ? 256 : 1024) norm_window_kernel(const
         }
       }
     }
-#pragma unroll
-    for (int k = 0; k < IT; ++k)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s[k][i] = next[k][i];
   }
 }
 
