@@ -197,11 +197,11 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormArgs a) {
   }
 }
 
-// Many rows: each CTA (two an SM where the ring fits) walks rows blockIdx.x +
-// i gridDim.x with `group` threads, IT vectors of 8 a thread; the rows of x and
-// residual come by bulk copies into a ring of `depth` stages, so that about
-// 200 KB an SM are in flight, and the weights stay in registers.  With one
-// row in flight a CTA the same rows moved at 4.5 TB/s.
+// Many rows: each CTA walks rows blockIdx.x + i gridDim.x, IT vectors of 8 a
+// thread; the rows of x and residual come by bulk copies into a ring of `depth`
+// stages, so that up to 200 KB an SM are in flight, and the weights stay in
+// registers.  4096 x 7168 with codes moves at 6.1 TB/s (0.92 of the measured
+// copy rate); with one row in flight a CTA it was 4.5 TB/s.
 template <int IT, bool XF32, int RES>
 __global__ void __launch_bounds__(1024) norm_rows_kernel(const NormArgs a, int depth, int* err) {
   extern __shared__ __align__(128) uint8_t smem[];
@@ -559,13 +559,18 @@ int launch_add_rms_norm(const void* x, int x_f32, const void* res, int res_f32, 
   if (vec) {
     // rows of 4 KB or more, at least two for every CTA of the ring kernel
     const int stage = H * ((x_f32 ? 4 : 2) + (r == 0 ? 0 : r == 1 ? 2 : 4));
-    const int it = nv <= 512 ? 1 : nv <= 2048 ? 2 : 4;
+    // One vector a thread up to 512 vectors; above, two, which leave room for a
+    // second CTA an SM, unless there are many rows of x and residual, where one
+    // (two CTAs in turn) was faster: 4096x7168 with codes 43 us, two 48; 640x7168
+    // 9.2 and 8.0; 4096x7168 without residual 26 and 20.  CTAs for about 1024
+    // threads an SM (4096x2048 with four 12.4 us, with two 17.2), rings of up to
+    // three rows (six without a residual).
+    const int it = nv <= 512 || (nv <= 1024 && r != 0 && T >= 8 * num_sms) ? 1 : nv <= 2048 ? 2 : 4;
     const int threads = ((nv + it - 1) / it + 31) / 32 * 32;
-    // as many CTAs as about 1024 threads and two stages each let on an SM
-    int ctas = 1024 / threads;
+    int ctas = threads <= 512 ? 1024 / threads : 2;
     while (ctas > 1 && ctas * 2 * stage > 220 * 1024) --ctas;
-    int depth = ctas > 0 ? 220 * 1024 / ctas / stage : 0;
-    if (depth > 4) depth = 4;
+    int depth = 220 * 1024 / ctas / stage;
+    if (depth > (r == 0 ? 6 : 3)) depth = r == 0 ? 6 : 3;
     if (stage >= 4096 && threads <= 1024 && depth >= 2 && T >= 2 * ctas * num_sms) {
       const int smem = depth * stage, grid = ctas * num_sms;
       return it == 1   ? launch_rows_types<1>(a, x_f32, r, threads, depth, smem, grid, nullptr, stream)
