@@ -320,11 +320,14 @@ __global__ void __launch_bounds__(kBalThreads, 1) balance_kernel(const BalanceAr
     if (threadIdx.x <= a.B) start0 = __ldg(a.starts + threadIdx.x);
     starts = starts_sm;
   }
-  if (a.ids) {  // this CTA's ids on their way 
+  if (a.ids) {  // this CTA's ids and mask on their way
     const char* p = reinterpret_cast<const char*>(a.ids + static_cast<size_t>(t0) * a.k);
     const size_t bytes = static_cast<size_t>(t1 - t0) * a.k * 4;
     for (size_t i = threadIdx.x * size_t{128}; i < bytes; i += THREADS * size_t{128})
       asm volatile("prefetch.global.L2 [%0];" ::"l"(p + i));
+    if (a.mask)
+      for (int i = t0 + threadIdx.x * 128; i < t1; i += THREADS * 128)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(a.mask + i));
   }
   if (a.starts && a.B < kBalStarts) {
     if (threadIdx.x <= a.B) starts_sm[threadIdx.x] = start0;
@@ -399,9 +402,29 @@ __global__ void __launch_bounds__(kBalThreads, 1) balance_kernel(const BalanceAr
       }
     }
     if (starts == starts_sm) __syncthreads();
-    // The CTA's tokens, up to kBalPieces sequences a pass (a CTA that took a
-    // pass for each held up the barrier by 2 us when most have one)
-    for (int t = t0; t < t1;) {
+    // A CTA whose tokens lie in more than kBalPieces sequences counts straight
+    // into the counters: its assignments spread over many of them (33 tokens in
+    // 16 sequences: a pass for every four took 25 us)
+    const int sfirst = t0 < t1 ? sequence_of(starts, a.B, t0) : -1;
+    const int slast = t0 < t1 ? sequence_of(starts, a.B, t1 - 1) : -1;
+    const bool spread = (slast < 0 ? a.B : slast + 1) - (sfirst < 0 ? 0 : sfirst) > kBalPieces;
+    if (spread) {
+      const unsigned n = static_cast<unsigned>(t1 - t0) * a.k;
+      const int32_t* ids = a.ids + static_cast<size_t>(t0) * a.k;
+      for (unsigned i = threadIdx.x; i < n; i += THREADS) {
+        const int e = __ldg(ids + i);
+        const int token = t0 + static_cast<int>(i / a.k);
+        const int b = sequence_of(starts, a.B, token);
+        if (b >= 0 && (!a.mask || a.mask[token] != 0)) {
+          if (e >= 0 && e < a.E) atomicAdd(cnt + static_cast<size_t>(b) * pitch + e, 1);
+          else bad = true;
+          if (i % a.k == 0) atomicAdd(tok + static_cast<size_t>(b) * tpitch, 1);
+        }
+      }
+    }
+    // Otherwise its sequences' counts in shared memory, in one pass (a CTA that
+    // took a pass for each held up the barrier by 2 us when most have one)
+    for (int t = spread ? t1 : t0; t < t1;) {
       int pb[kBalPieces], pe[kBalPieces];  // a piece's sequence and end
       int end = t, np = 0;
 #pragma unroll
@@ -782,6 +805,7 @@ int launch_one(BalanceArgs a, int num_sms, cudaStream_t st) {
   }
   a.chunk = static_cast<int>((static_cast<long long>(a.T) + grid - 1) / grid);
   a.cluster = cluster > 1;
+  if (grid == 1) a.acc = nullptr;  // one CTA clears counts and tokens itself and adds to them
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   cfg.gridDim = dim3(grid);

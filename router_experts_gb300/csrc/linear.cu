@@ -129,6 +129,7 @@ __global__ void __launch_bounds__(32 * kTokMaxWarps, 2)
   const int S = a.splits;
   const int s = static_cast<int>(cluster_ctarank());
   const int n0 = blockIdx.x / S * (GATED ? 8 : 16);
+  const int t0 = blockIdx.y * COLS;
   if (S > 1) cluster_arrive();
   grid_dependency_launch();
   grid_dependency_wait();
@@ -169,7 +170,7 @@ __global__ void __launch_bounds__(32 * kTokMaxWarps, 2)
         const int k = cd * kBK + 32 * h + 8 * q;
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-          const int t = 8 * j + g;
+          const int t = t0 + 8 * j + g;
           xv[j][h] = cd < c1 && k < a.K && t < a.T
                          ? __ldg(reinterpret_cast<const uint4*>(x + static_cast<size_t>(t) * a.K + k))
                          : zero;
@@ -212,12 +213,12 @@ __global__ void __launch_bounds__(32 * kTokMaxWarps, 2)
     if (s != 0) return;
   }
   for (int i = threadIdx.x; i < 16 * COLS; i += blockDim.x) {
-    const int r = i & 15, t = i >> 4;
+    const int r = i & 15, tc = i >> 4, t = t0 + tc;
     float v = 0.f;
     if (S > 1) {
       for (int k = 0; k < S; ++k) v += recv[k][i];
     } else {
-      for (int k = 0; k < warps; ++k) v += part[k][r][t];
+      for (int k = 0; k < warps; ++k) v += part[k][r][tc];
     }
     // gated: rows 8..15 are the up sums of rows 0..7, eight lanes on
     const float u = GATED ? __shfl_down_sync(0xffffffffu, v, 8) : 0.f;
@@ -595,11 +596,11 @@ MOE_DEV void chunk_finish(const LinearArgs& a, int trow0, int n, float* staged, 
   const int lane = threadIdx.x & 31;
   if (a.bias) {
 #pragma unroll
-    for (int c = 0; c < 16; ++c)
-      if (VEC || n + c < a.N) {
-        v[c] += __ldg(a.bias + n + c);
-        if constexpr (GATED) u[c] += __ldg(a.bias + a.N + n + c);
-      }
+    for (int c = 0; c < 16; ++c) {
+      const int at = VEC ? n + c : min(n + c, a.N - 1);
+      v[c] += __ldg(a.bias + at);
+      if constexpr (GATED) u[c] += __ldg(a.bias + a.N + at);
+    }
   }
 #pragma unroll
   for (int c = 0; c < 16; ++c) v[c] = activate(ACT, v[c], GATED ? u[c] : 0.f);
@@ -1022,7 +1023,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 // ---------------------------------------------------------------------------
 // Cluster launch that may start before the kernel in front of it has ended.
 template <class Kernel, class... Args>
-int launch_cluster(Kernel kernel, int cluster, int grid, int threads, int smem,
+int launch_cluster(Kernel kernel, int cluster, dim3 grid, int threads, int smem,
                    cudaStream_t stream, Args... args) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
@@ -1032,7 +1033,7 @@ int launch_cluster(Kernel kernel, int cluster, int grid, int threads, int smem,
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -1044,8 +1045,8 @@ int launch_cluster(Kernel kernel, int cluster, int grid, int threads, int smem,
 
 template <int ACT, int NT>
 int launch_token(const void* x, const void* w, const LinearArgs& a, cudaStream_t stream) {
-  return launch_cluster(linear_token_kernel<ACT, NT>, a.splits, a.tiles_n * a.splits, 32 * a.bn, 0,
-                        stream, static_cast<const __nv_bfloat16*>(x),
+  return launch_cluster(linear_token_kernel<ACT, NT>, a.splits,
+                        dim3(a.tiles_n * a.splits, a.tiles_t), 32 * a.bn, 0, stream, static_cast<const __nv_bfloat16*>(x),
                         static_cast<const __nv_bfloat16*>(w), a);
 }
 template <int NT>
@@ -1064,7 +1065,7 @@ int launch_row(const CUtensorMap& tw, const CUtensorMap& tx, const LinearArgs& a
   static std::atomic<unsigned long long> smem_set{0};
   const auto kernel = linear_row_kernel<ACT, BN>;
   if (!ensure_smem_limit(reinterpret_cast<const void*>(kernel), C::SMEM_BYTES, smem_set)) return -1;
-  return launch_cluster(kernel, a.splits, a.tiles_n * a.tiles_t * a.splits, C::THREADS,
+  return launch_cluster(kernel, a.splits, dim3(a.tiles_n * a.tiles_t * a.splits), C::THREADS,
                         C::SMEM_BYTES, stream, tw, tx, a);
 }
 
@@ -1085,7 +1086,7 @@ int launch_pair(const CUtensorMap& tw, const CUtensorMap& tx, const LinearArgs& 
   if (a.splits > 1) {
     const auto kernel = linear_pair_kernel<ACT, VEC, true, false>;
     if (!ensure_smem_limit(reinterpret_cast<const void*>(kernel), kPairSmem, split_set)) return -1;
-    return launch_cluster(kernel, 2 * a.splits, 2 * a.splits * tiles, kPairThreads, kPairSmem,
+    return launch_cluster(kernel, 2 * a.splits, dim3(2 * a.splits * tiles), kPairThreads, kPairSmem,
                           stream, tw, tx, a);
   }
   const auto kernel = a.out_f32 ? linear_pair_kernel<ACT, VEC, false, true>
@@ -1094,7 +1095,7 @@ int launch_pair(const CUtensorMap& tw, const CUtensorMap& tx, const LinearArgs& 
                          a.out_f32 ? wide_set : whole_set))
     return -1;
   const int pairs = tiles < num_sms / 2 ? tiles : num_sms / 2;
-  return launch_cluster(kernel, 2, 2 * pairs, kPairThreads, kPairSmem, stream, tw, tx, a);
+  return launch_cluster(kernel, 2, dim3(2 * pairs), kPairThreads, kPairSmem, stream, tw, tx, a);
 }
 template <bool VEC>
 int launch_pair_act(int act, const CUtensorMap& tw, const CUtensorMap& tx, const LinearArgs& a,
@@ -1107,6 +1108,10 @@ int launch_pair_act(int act, const CUtensorMap& tw, const CUtensorMap& tx, const
 
 }  // namespace
 
+// Weight bytes that the token kernel may read in all above 16 tokens (128 x 512
+// x 512, 4.2 MB: 3.4 us, row tiles 5.4; 24 x 2048 x 1024, 8.4 MB: 4.9 and 4.1).
+constexpr long long kTokenBytes = 4 << 20;
+
 // Estimated cycles of every tiling, and the cheapest.  Measured on GB300: an
 // SM takes in about 57 bytes a cycle from L2, a ring turns over in about 2300
 // cycles when it streams from HBM, a K step costs its issuing warp about 380
@@ -1117,14 +1122,18 @@ int launch_pair_act(int act, const CUtensorMap& tw, const CUtensorMap& tx, const
 LinearPlan plan_linear(int T, int K, int N, bool gated, bool out_f32, int num_sms) {
   LinearPlan best{};
   const int KB = (K + kBK - 1) / kBK;
-  if (T <= 16) {
+  // Up to 16 tokens; more, in groups of 16 that each read the weights from L2,
+  // while that is little.
+  const long long groups = (T + 15) / 16;
+  if (T <= 16 || (T <= 512 && groups * N * K * (gated ? 4 : 2) <= kTokenBytes)) {
     // a CTA has 4 or 8 pieces in flight a warp; K is split only when there are
     // fewer tiles than SMs
     best.kind = kLinearToken;
     best.tiles_n = (N + (gated ? 7 : 15)) / (gated ? 8 : 16);
-    best.tiles_t = 1;
+    best.tiles_t = static_cast<int>(groups);
     best.splits = 1;
-    while (best.splits < 8 && best.tiles_n * best.splits < num_sms && KB / (2 * best.splits) >= 8)
+    while (best.splits < 8 && best.tiles_n * best.tiles_t * best.splits < num_sms &&
+           KB / (2 * best.splits) >= 8)
       best.splits *= 2;
     best.bn = KB / best.splits >= 64 ? 8 : 4;
     return best;
@@ -1156,8 +1165,10 @@ LinearPlan plan_linear(int T, int K, int N, bool gated, bool out_f32, int num_sm
       const double units = static_cast<double>(tn) * tt * s;
       const double share = bn == 128 || units <= num_sms ? 1.0 : 2.0;  // CTAs of an SM
       const double step = fmax(fmax(stage * share / ingest, turn / ring), issue);
-      const double run = ceil(units / fit) * ((KB + s - 1) / s) * step;
-      consider(kLinearRow, bn, s, tn, tt, fmax(run, hbm) + 6000 + (s > 1 ? 1500 : 0) + 8.0 * bn);
+      // a CTA's start and end are hidden behind another's from two an SM on
+      const double waves = ceil(units / fit), fixed = 6000 + (s > 1 ? 1500 : 0) + 8.0 * bn;
+      const double run = waves * ((KB + s - 1) / s) * step + (waves - 1) * fixed / (fit / num_sms);
+      consider(kLinearRow, bn, s, tn, tt, fmax(run, hbm) + fixed);
     }
   }
   if (T > 64) {

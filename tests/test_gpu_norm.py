@@ -68,7 +68,8 @@ def check(x, r, w, eps, got):
 @pytest.mark.parametrize("T,H", [
     (1, 1), (3, 2), (5, 7), (2, 8), (9, 31), (4, 40), (7, 64), (3, 257), (33, 1000), (5, 1001),
     (130, 2045), (1, 2048), (64, 4096), (2, 4100), (700, 4096), (1, 7168), (5, 7168), (300, 7168),
-    (3, 8200), (2, 9001), (2, 16384), (2, 20008), (3, 40000), (1, 70001)])
+    (3, 8200), (2, 9001), (2, 16384), (2, 20008), (3, 40000), (1, 70001), (700, 2048),
+    (1300, 7168), (620, 16384), (640, 32768), (2000, 2001), (1500, 1031), (500, 8193)])
 def test_rows(T, H):
     x, r, w = make(T, H, seed=T + H)
     check(x, r, w, 1e-6, moe.add_rms_norm(x, w, r, 1e-6))
@@ -84,7 +85,8 @@ def test_types(x_dt, res_dt, w_dt, T, H):
 
 
 @pytest.mark.parametrize("T,H", [(1, 32), (3, 64), (2, 96), (17, 1056), (1, 4096), (64, 4096),
-                                 (1, 7168), (600, 7168), (2, 8224), (3, 33024), (3, 40992)])
+                                 (1, 7168), (600, 7168), (1300, 7168), (1250, 4096), (2500, 1056), (2, 8224),
+                                 (3, 33024), (3, 40992)])
 @pytest.mark.parametrize("y", [False, True])
 def test_e4m3(T, H, y):
     x, r, w = make(T, H, seed=T * 7 + H)
@@ -118,8 +120,9 @@ def test_unaligned_rows():
         moe.add_rms_norm(flat[0], w1, flat[1], 1e-6, e4m3=True)
 
 
-def test_in_place_residual():
-    x, r, w = make(40, 2048, seed=9)
+@pytest.mark.parametrize("T,H", [(40, 2048), (40, 2045), (1300, 1003), (2000, 2048), (1400, 7168)])
+def test_in_place_residual(T, H):
+    x, r, w = make(T, H, seed=9)
     want = moe.add_rms_norm(x, w, r, 1e-6)
     y = torch.empty_like(x)
     mine = r.clone()
