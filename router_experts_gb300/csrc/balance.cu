@@ -129,42 +129,6 @@ MOE_DEV Pair warp_pair_sum(Pair v) {
   return v;
 }
 
-MOE_DEV float rcp_approx(float x) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
-// Two values at a time: an instruction of the f32x2 kind does both (the token
-// loop is bound by its instructions, not by memory, without them).
-struct Two {
-  unsigned long long v;
-};
-MOE_DEV Two two(float a, float b) {
-  Two r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
-  return r;
-}
-MOE_DEV Two two(float a) { return two(a, a); }
-MOE_DEV void split(Two x, float* a, float* b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(*a), "=f"(*b) : "l"(x.v));
-}
-MOE_DEV Two mul2(Two a, Two b) {
-  Two r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-MOE_DEV Two add2(Two a, Two b) {
-  Two r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-MOE_DEV Two fma2(Two a, Two b, Two c) {
-  Two r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
-
 // e^x for x <= 0 as 2^y: y = x log2(e) in two parts, the hardware's power of
 // two for the first and 1 + z ln 2 for the second (|z| < 2^-16), so that the
 // relative error stays near 2^-22 however small the result is.  Below -120 it
