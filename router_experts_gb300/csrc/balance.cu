@@ -367,8 +367,9 @@ __global__ void __launch_bounds__(kBalThreads, 1) balance_kernel(const BalanceAr
     }
     if (starts == starts_sm) __syncthreads();
     // A CTA whose tokens lie in more than kBalPieces sequences counts straight
-    // into the counters: its assignments spread over many of them (33 tokens in
-    // 16 sequences: a pass for every four took 25 us)
+    // into the counters: its assignments spread over many of them (256 experts,
+    // passes of four sequences against this: 33 tokens in 16 sequences 22.4 and
+    // 9.1 us, 2048 in 128 20.1 and 17.3, 65536 in 1024 62 and 50)
     const int sfirst = t0 < t1 ? sequence_of(starts, a.B, t0) : -1;
     const int slast = t0 < t1 ? sequence_of(starts, a.B, t1 - 1) : -1;
     const bool spread = (slast < 0 ? a.B : slast + 1) - (sfirst < 0 ? 0 : sfirst) > kBalPieces;
